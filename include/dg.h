@@ -397,6 +397,158 @@ int dg_vocab_attention_static(int32_t C, int32_t V, int32_t d, int32_t dtype, fl
                               const void* E, const void* h, float* H, int32_t* argmax,
                               float* sc, void* stream);
 
+/* ------------------------------------------------------------------------- */
+/*
+ * Attention-layer operators for a caller's own backbone. [VG] 4 and [EX]
+ * describe it: a causal prefill and a bidirectional denoise over the canvas,
+ * both reading one key/value cache that grows by a canvas per block. The pages
+ * give no kernels; these four calls are a layer's work between its linear
+ * projections:
+ *   dg_qk_norm_rope     norms the query and key heads and rotates them
+ *   dg_cache_write      puts the new tokens' keys and values into the cache
+ *   dg_cache_attention  attends over the cache, the new tokens included
+ *   dg_cache_read       takes rows back out of the cache as plain arrays
+ * They need no context. All pointers are device pointers of the current
+ * device; every call is asynchronous on `stream` (NULL = legacy default
+ * stream), allocates nothing, can be captured into a graph, and reports errors
+ * through dg_last_error(NULL). Pointers are 16-byte aligned, strides are in
+ * elements and multiples of 8 (rows are read 16 bytes at a time). Sizes of
+ * zero are allowed and launch nothing.
+ */
+
+/*
+ * RMS norm of every query and key head, then the rotation by position:
+ *   y = x / sqrt(mean(x^2) + eps) * (weight + weight_offset)
+ *   (y_a, y_b) -> (y_a cos t - y_b sin t, y_b cos t + y_a sin t)
+ * with t = positions[token] * inv_freq[i] for the pairs i < rot_dim / 2:
+ * (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved != 0.
+ * Elements from rot_dim on are only normed. Computed in fp32 and rounded once;
+ * the angle is right to 2^-25 turns at every int32 position (|inv_freq| < 1000).
+ *   tokens, q_heads, k_heads >= 0; head_dim a multiple of 8, 8..256; rot_dim a
+ *   multiple of 16, 0..head_dim; dtype DG_F32 or DG_BF16 (q, k, weights, outputs).
+ *   q, k          [tokens][heads][head_dim], element strides q_token_stride,
+ *                 q_head_stride, ... (head_dim contiguous).
+ *   q_weight, k_weight  [head_dim], or NULL for ones.
+ *   positions     int32 [tokens] (may be negative); inv_freq double [rot_dim / 2],
+ *                 radians per position.
+ *   q_out, k_out  [tokens][heads][head_dim] contiguous; q_out may be q itself
+ *                 when q is contiguous (same for k), and must not overlap an
+ *                 input otherwise.
+ * Errors: DG_EINVAL, DG_EUNSUPPORTED (head_dim, rot_dim), DG_ECUDA.
+ */
+int dg_qk_norm_rope(int32_t tokens, int32_t q_heads, int32_t k_heads, int32_t head_dim,
+                    int32_t rot_dim, int32_t interleaved, int32_t dtype,
+                    const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                    const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                    const void* q_weight, const void* k_weight, float weight_offset, float eps,
+                    const int32_t* positions, const double* inv_freq,
+                    void* q_out, void* k_out, void* stream);
+
+/* How a cache holds keys and values. */
+#define DG_KV_BF16  0        /* bf16                                           */
+#define DG_KV_E4M3  1        /* e4m3 codes, one power-of-two scale per row     */
+
+/*
+ * A paged key/value cache, caller-owned. A row is one token's head_dim values
+ * for one head; row (page, head, offset) of k and v:
+ *   k, v          bf16 or e4m3 codes, [pages][kv_heads][page_size][head_dim]
+ *   k_exp, v_exp  uint8 [pages][kv_heads][page_size], DG_KV_E4M3 only: the
+ *                 row's value is code * 2^(exp - 127). The exponent is the
+ *                 smallest that brings the row's largest finite magnitude
+ *                 within 448 (127 for a row of zeros; held to -100..119);
+ *                 codes round to nearest even, saturated. e4m3 has no
+ *                 infinity: infinities and NaN are written as NaN.
+ *   status        int32 device word, caller-owned, zeroed by the caller: a call
+ *                 that meets a page outside [0, pages), or a position outside
+ *                 the page table, skips the row (reads: zeros; attention takes
+ *                 zero keys and values, and such a past as the nearest that
+ *                 fits) and sets it to DG_EINVAL; a device wait that runs out
+ *                 sets DG_ETIMEOUT.
+ * head_dim: a multiple of 16, 16..256; page_size >= 1; fewer than 2^31 rows.
+ */
+typedef struct dg_kv_cache {
+  void*    k;
+  void*    v;
+  uint8_t* k_exp;
+  uint8_t* v_exp;
+  int32_t* status;
+  int32_t  pages, page_size, kv_heads, head_dim;
+  int32_t  format;            /* DG_KV_*                                        */
+} dg_kv_cache;
+
+/*
+ * Which tokens a call is about: sequence b of the batch has the tokens (rows of
+ * q, k, v) first[b] .. first[b+1]-1, at the positions past[b], past[b]+1, ...
+ * of its cache; position p lies in page page_table[b][p / page_size]. Rows from
+ * first[batch] on (padding) are left as they are. All arrays are device int32,
+ * read when the kernels run, so that a captured graph can be replayed with new
+ * lengths. Sequences may share pages that are only read; a page that a call
+ * writes belongs to one sequence.
+ */
+typedef struct dg_kv_batch {
+  const int32_t* page_table;  /* [batch][table_stride]                          */
+  const int32_t* first;       /* [batch + 1], from 0, non-decreasing            */
+  const int32_t* past;        /* [batch], >= 0                                  */
+  int32_t batch;              /* sequences, 0..1024                             */
+  int32_t table_stride;       /* pages per sequence in page_table               */
+  int32_t tokens;             /* rows of q, k, v, outputs (first[batch] <= it)  */
+} dg_kv_batch;
+
+/*
+ * Write the batch's tokens into the cache. k and v: [tokens][kv_heads][head_dim]
+ * of dtype (DG_F32 or DG_BF16) with element strides; a bf16 cache takes fp32
+ * values rounded to nearest even. One launch.
+ */
+int dg_cache_write(const dg_kv_cache* cache, const dg_kv_batch* batch, int32_t dtype,
+                   const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                   const void* v, int64_t v_token_stride, int64_t v_head_stride, void* stream);
+
+/*
+ * Read the batch's tokens out of the cache: k_out and v_out, contiguous
+ * [tokens][kv_heads][head_dim] of dtype (DG_F32 or DG_BF16; both hold every
+ * e4m3 row exactly). One launch.
+ */
+int dg_cache_read(const dg_kv_cache* cache, const dg_kv_batch* batch, int32_t dtype,
+                  void* k_out, void* v_out, void* stream);
+
+/* Which of its sequence's new tokens a new token sees (all see the past). */
+#define DG_MASK_FULL    0    /* every one: a canvas ([VG] 4, bidirectional)    */
+#define DG_MASK_CAUSAL  1    /* itself and those before it: prompts, one token */
+#define DG_MASK_TREE    2    /* those whose bit is set: drafts to be verified  */
+
+/*
+ * Attention of the batch's tokens over the cache, which holds their own keys
+ * and values already (dg_cache_write): for token i of sequence b and query head
+ * h, over the positions j that it sees,
+ *   out = sum_j p_j v_j,  p = softmax_j(scale q.k_j),  lse = log sum_j e^(scale q.k_j)
+ * with keys and values of head h / (q_heads / kv_heads).
+ *   q        bf16 [tokens][q_heads][head_dim] with element strides; q_heads a
+ *            multiple of kv_heads.
+ *   scale    > 0, finite.
+ *   mask     DG_MASK_*. DG_MASK_TREE: tree_mask, uint32 [tokens][mask_words];
+ *            token i sees new token j of its sequence if bit j % 32 of word
+ *            j / 32 of its row is set (itself included; words beyond
+ *            mask_words count as zero).
+ *   out      bf16 [tokens][q_heads][head_dim], contiguous; a token that sees
+ *            nothing gets zeros. lse: float [tokens][q_heads] or NULL
+ *            (-infinity where nothing is seen).
+ *   scratch  device, >= dg_cache_attention_scratch_bytes(...) bytes, 256-byte
+ *            aligned; holds nothing from one call to the next. Calls that may
+ *            overlap on the GPU need one each.
+ * What a token does not see does not touch its result, infinities and NaN
+ * included. Products take bf16 operands (an e4m3 row is exact in bf16) with
+ * fp32 accumulation; the softmax and its sums are fp32; probabilities are
+ * rounded to bf16 for the second product.
+ * Errors: DG_EINVAL, DG_ENOMEM (scratch), DG_EUNSUPPORTED (head_dim, batch,
+ * row count), DG_ECUDA.
+ */
+size_t dg_cache_attention_scratch_bytes(const dg_kv_cache* cache, const dg_kv_batch* batch,
+                                        int32_t q_heads);
+int dg_cache_attention(const dg_kv_cache* cache, const dg_kv_batch* batch, int32_t q_heads,
+                       const void* q, int64_t q_token_stride, int64_t q_head_stride, float scale,
+                       int32_t mask, const uint32_t* tree_mask, int32_t mask_words,
+                       void* out, float* lse, void* scratch, size_t scratch_bytes, void* stream);
+
 /* Release the context (host memory and graph objects only). */
 int dg_free(dg_ctx* ctx);
 

@@ -17,6 +17,8 @@ Modules:
              adaptive stop, the step and the block loop.
   fp8     -- e4m3/e5m2 rounding, per-row power-of-two scaling and the step's
              vocabulary attention with a narrow (e4m3) embedding.
+  attention -- the attention-layer operators: head norms with rotation, the
+             rows of a paged cache, attention under a mask.
 
 Parity status: every function is pinned by tests/test_oracle_*.py against
 closed forms, brute force in long double, a published SplitMix64 vector, a
@@ -25,4 +27,4 @@ conversion. The pages' end-to-end quality behaviour
 (quality versus step count, the Sudoku experiment) needs the trained model and
 is not part of this oracle.
 """
-from . import rng, method, fp8  # noqa: F401
+from . import rng, method, fp8, attention  # noqa: F401

@@ -25,6 +25,8 @@ DG_ACCEPT_CUMSUM, DG_ACCEPT_MINUS_MAX = 0, 1
 DG_IMPL_AUTO, DG_IMPL_SIMT, DG_IMPL_TC = 0, 1, 2
 DG_TOKEN_ARGMAX, DG_TOKEN_MULTINOMIAL = 0, 1
 DG_E_NATIVE, DG_E_FP8 = 0, 1
+DG_KV_BF16, DG_KV_E4M3 = 0, 1
+DG_MASK_FULL, DG_MASK_CAUSAL, DG_MASK_TREE = 0, 1, 2
 (DG_CANVAS, DG_ARGMAX, DG_ENTROPY, DG_ACCEPT, DG_SC, DG_HIDDEN, DG_TARGET, DG_ORDER, DG_PREFIX,
  DG_STATE, DG_MREF, DG_SAMPLED, DG_EMIT, DG_CANVAS_STATE, DG_TC_TRACE_COUNTERS) = range(15)
 DG_ST_T, DG_ST_BLOCK, DG_ST_UNCHANGED, DG_ST_DONE, DG_ST_STEPS, DG_ST_K, DG_ST_STATUS, \
@@ -46,6 +48,19 @@ class dg_config(ctypes.Structure):
         ("shard_v0", ctypes.c_int32), ("shard_nv", ctypes.c_int32),
         ("e_format", ctypes.c_int32),
     ]
+
+
+class dg_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("status", ctypes.c_void_p), ("pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class dg_kv_batch(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("first", ctypes.c_void_p),
+                ("past", ctypes.c_void_p), ("batch", ctypes.c_int32),
+                ("table_stride", ctypes.c_int32), ("tokens", ctypes.c_int32)]
 
 
 class DgError(RuntimeError):
@@ -92,6 +107,16 @@ def lib():
     L.dg_denoise_step_partial.argtypes = [_P, _P]
     L.dg_denoise_step_finish.argtypes = [_P, _P]
     L.dg_tc_schedule.argtypes = [_I, _I, _I, _I, _P, _I]
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    kvp = [ctypes.POINTER(dg_kv_cache), ctypes.POINTER(dg_kv_batch)]
+    L.dg_qk_norm_rope.argtypes = [_I] * 7 + [_P, i64, i64, _P, i64, i64, _P, _P, f32, f32, _P, _P,
+                                             _P, _P, _P]
+    L.dg_cache_write.argtypes = kvp + [_I, _P, i64, i64, _P, i64, i64, _P]
+    L.dg_cache_read.argtypes = kvp + [_I, _P, _P, _P]
+    L.dg_cache_attention_scratch_bytes.argtypes = kvp + [_I]
+    L.dg_cache_attention_scratch_bytes.restype = ctypes.c_size_t
+    L.dg_cache_attention.argtypes = kvp + [_I, _P, i64, i64, f32, _I, _P, _I, _P, _P, _P,
+                                           ctypes.c_size_t, _P]
     L.dg_free.argtypes = [_P]
     L.dg_last_error.argtypes = [_P]
     L.dg_last_error.restype = ctypes.c_char_p
@@ -99,7 +124,8 @@ def lib():
                  "dg_denoise_block", "dg_read", "dg_write", "dg_profile", "dg_profile_read",
                  "dg_impl", "dg_free", "dg_vocab_attention_static", "dg_denoise_step_partial",
                  "dg_denoise_step_finish", "dg_tc_schedule", "dg_inject_stall",
-                 "dg_self_condition"):
+                 "dg_self_condition", "dg_qk_norm_rope", "dg_cache_write", "dg_cache_read",
+                 "dg_cache_attention"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -228,6 +254,49 @@ def dg_self_condition(ctx, d_ff: int, W1_ptr: int, b1_ptr: int, W2_ptr: int, b2_
     """emb += W2 gelu(W1 sc + b1) + b2 on the context's stream (see include/dg.h)."""
     _check(lib().dg_self_condition(ctx, d_ff, _P(W1_ptr), _P(b1_ptr), _P(W2_ptr), _P(b2_ptr),
                                    _P(emb_ptr), emb_dtype, _P(scratch_ptr)), ctx)
+
+
+def dg_qk_norm_rope(tokens: int, q_heads: int, k_heads: int, head_dim: int, rot_dim: int,
+                    interleaved: bool, dtype: int, q_ptr: int, q_token_stride: int,
+                    q_head_stride: int, k_ptr: int, k_token_stride: int, k_head_stride: int,
+                    q_weight_ptr: int, k_weight_ptr: int, weight_offset: float, eps: float,
+                    positions_ptr: int, inv_freq_ptr: int, q_out_ptr: int, k_out_ptr: int,
+                    stream_ptr: int) -> None:
+    """Norm and rotate query and key heads (see include/dg.h)."""
+    _check(lib().dg_qk_norm_rope(tokens, q_heads, k_heads, head_dim, rot_dim,
+                                 1 if interleaved else 0, dtype, q_ptr, q_token_stride,
+                                 q_head_stride, k_ptr, k_token_stride, k_head_stride, q_weight_ptr,
+                                 k_weight_ptr, weight_offset, eps, positions_ptr, inv_freq_ptr,
+                                 q_out_ptr, k_out_ptr, stream_ptr), None)
+
+
+def dg_cache_write(cache: dg_kv_cache, batch: dg_kv_batch, dtype: int, k_ptr: int,
+                   k_token_stride: int, k_head_stride: int, v_ptr: int, v_token_stride: int,
+                   v_head_stride: int, stream_ptr: int) -> None:
+    _check(lib().dg_cache_write(ctypes.byref(cache), ctypes.byref(batch), dtype, k_ptr,
+                                k_token_stride, k_head_stride, v_ptr, v_token_stride, v_head_stride,
+                                stream_ptr), None)
+
+
+def dg_cache_read(cache: dg_kv_cache, batch: dg_kv_batch, dtype: int, k_out_ptr: int,
+                  v_out_ptr: int, stream_ptr: int) -> None:
+    _check(lib().dg_cache_read(ctypes.byref(cache), ctypes.byref(batch), dtype, k_out_ptr, v_out_ptr,
+                               stream_ptr), None)
+
+
+def dg_cache_attention_scratch_bytes(cache: dg_kv_cache, batch: dg_kv_batch, q_heads: int) -> int:
+    return int(lib().dg_cache_attention_scratch_bytes(ctypes.byref(cache), ctypes.byref(batch), q_heads))
+
+
+def dg_cache_attention(cache: dg_kv_cache, batch: dg_kv_batch, q_heads: int, q_ptr: int,
+                       q_token_stride: int, q_head_stride: int, scale: float, mask: int,
+                       tree_mask_ptr: int, mask_words: int, out_ptr: int, lse_ptr: int,
+                       scratch_ptr: int, scratch_bytes: int, stream_ptr: int) -> None:
+    """Attention of a batch of new tokens over a paged cache (see include/dg.h)."""
+    _check(lib().dg_cache_attention(ctypes.byref(cache), ctypes.byref(batch), q_heads, q_ptr,
+                                    q_token_stride, q_head_stride, scale, mask, tree_mask_ptr,
+                                    mask_words, out_ptr, lse_ptr, scratch_ptr, scratch_bytes,
+                                    stream_ptr), None)
 
 
 def dg_inject_stall(ctx, wait_limit_ns: int, stall: int) -> None:
@@ -414,3 +483,18 @@ def allreduce_partials(buf, C: int, d: int, group=None) -> None:
     keys.bitwise_xor_(-(1 << 63))
     dist.all_reduce(keys, op=dist.ReduceOp.MAX, group=group)
     keys.bitwise_xor_(-(1 << 63))
+
+
+# The attention-layer operators on torch tensors live in a module of their own
+# and are loaded on first use, so that importing the package needs no torch.
+_ATTENTION = ("KVBatch", "KVCache", "qk_norm_rope", "rope_frequencies")
+
+
+def __getattr__(name):
+    if name in _ATTENTION:
+        from . import attention
+
+        for n in _ATTENTION:
+            globals()[n] = getattr(attention, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

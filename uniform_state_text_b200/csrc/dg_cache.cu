@@ -1,0 +1,430 @@
+// Row operators of an attention layer: per-head norms with rotation
+// (dg_qk_norm_rope), and the paged key/value cache's write and read
+// (dg_cache_write, dg_cache_read).
+//
+// All three are bound by memory: each element is read once and written once,
+// with a few operations between. A row (one token, one head) belongs to a
+// group of 8, 16 or 32 lanes (head_dim up to 64, 128, 256), 8 elements to a
+// lane, so that a row is one fully used memory transaction per lane and its
+// sums and maxima are a few shuffles; nothing passes through shared memory.
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "dg.h"
+#include "dg_cache.cuh"
+#include "dg_fp8.cuh"
+
+namespace dg {
+void set_last_error(const char* msg);   // dg_api.cu: the message dg_last_error(NULL) returns
+}
+
+namespace dg {
+namespace rows {
+
+constexpr int THREADS = 256;
+
+// 8 elements as fp32.
+template <typename T> __device__ __forceinline__ void load8(const T* p, float* v);
+template <> __device__ __forceinline__ void load8<float>(const float* p, float* v) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* v) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+template <typename T> __device__ __forceinline__ void store8(T* p, const float* v);
+template <> __device__ __forceinline__ void store8<float>(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float* v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+    w[j] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ---------------------------------------------------------------------------
+// Norm and rotation.
+// ---------------------------------------------------------------------------
+struct NormArgs {
+  const void *q, *k, *wq, *wk;
+  void *qo, *ko;
+  int64_t q_ts, q_hs, k_ts, k_hs;
+  const int32_t* pos;
+  const double* freq;
+  int tokens, qh, kh, D, rot, chunk, nchunk;   // chunk: heads per group, nchunk: groups per token
+  float off, eps;
+};
+
+// The fraction of a turn per position as a 64-bit fixed-point number: its
+// product with an integer position, mod 2^64, is the phase itself, with no
+// range reduction. 1 / (2 pi) is taken in two doubles and the product's
+// rounding is kept, so that the fraction is right to 2^-63 turns and the phase
+// to 2^-32 turns at any int32 position.
+__device__ __forceinline__ uint64_t turns_per_position(double radians) {
+  const double hi = radians * 0.15915494309189535;
+  const double lo = fma(radians, 0.15915494309189535, -hi) + radians * -9.839338337591243e-18;
+  const double t = hi - floor(hi);
+  return (uint64_t)(t * 18446744073709551616.0) + (uint64_t)(int64_t)(lo * 18446744073709551616.0);
+}
+__device__ __forceinline__ void sincos_turns(uint64_t phase, float* s, float* c) {
+  // the top 32 bits, signed, as multiples of pi in [-1, 1); the rounding to
+  // fp32 moves the angle by at most pi 2^-25
+  sincospif((float)(int32_t)(uint32_t)(phase >> 32) * 4.656612873077392578125e-10f, s, c);
+}
+
+// One group of LPR lanes takes `chunk` heads of one token: its lanes' cosines
+// and sines are computed once and serve all of them.
+template <typename T, int LPR, bool INTERLEAVED>
+__global__ void __launch_bounds__(THREADS) k_norm_rope(const NormArgs a) {
+  const int64_t unit = ((int64_t)blockIdx.x * THREADS + threadIdx.x) / LPR;
+  const int token = (int)(unit / a.nchunk);
+  const int sub = threadIdx.x % LPR;
+  const bool live = token < a.tokens;               // whole groups; dead ones still shuffle
+  const int h0 = (int)(unit % a.nchunk) * a.chunk;
+  const int nh = live ? min(a.chunk, a.qh + a.kh - h0) : 0;
+  const int x0 = sub * 8;
+  const bool in = x0 < a.D;
+  const bool turn = x0 < a.rot;
+  const int half = a.rot / 2;
+  // this lane's rotations: 8 pairs with the other half's lane, or 4 of its own
+  float cs[INTERLEAVED ? 4 : 8], sn[INTERLEAVED ? 4 : 8];
+  if (turn && live) {
+    const int64_t pos = __ldg(a.pos + token);
+    const int p0 = INTERLEAVED ? x0 / 2 : (x0 < half ? x0 : x0 - half);
+#pragma unroll
+    for (int j = 0; j < (INTERLEAVED ? 4 : 8); ++j)
+      sincos_turns((uint64_t)pos * turns_per_position(__ldg(a.freq + p0 + j)), &sn[j], &cs[j]);
+  }
+  const int warp_lane = threadIdx.x & 31;
+  const int base = warp_lane - sub;                 // the group's first lane
+  const int mate = turn ? base + (x0 < half ? sub + half / 8 : sub - half / 8) : warp_lane;
+  // all groups of a warp run the same number of rounds, so that every lane shuffles
+  const int rounds = __reduce_max_sync(0xffffffffu, nh);
+  for (int r = 0; r < rounds; ++r) {
+    const bool on = r < nh && in;
+    const int h = h0 + r;
+    const bool is_q = h < a.qh;
+    const int hh = is_q ? h : h - a.qh;
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, w[8];
+    if (on) {
+      const T* src = is_q ? static_cast<const T*>(a.q) + token * a.q_ts + hh * a.q_hs
+                          : static_cast<const T*>(a.k) + token * a.k_ts + hh * a.k_hs;
+      load8(src + x0, v);
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+#pragma unroll
+    for (int m = LPR / 2; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+    const float rs = 1.0f / sqrtf(ss / (float)a.D + a.eps);
+    const T* wp = static_cast<const T*>(is_q ? a.wq : a.wk);
+    if (on && wp) load8(wp + x0, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = v[j] * rs * ((wp && on ? w[j] : 1.0f) + a.off);
+    if constexpr (INTERLEAVED) {
+      if (turn) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x = v[2 * j], y = v[2 * j + 1];
+          v[2 * j] = x * cs[j] - y * sn[j];
+          v[2 * j + 1] = y * cs[j] + x * sn[j];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float o = __shfl_sync(0xffffffffu, v[j], mate);
+        if (turn) v[j] = x0 < half ? v[j] * cs[j] - o * sn[j] : v[j] * cs[j] + o * sn[j];
+      }
+    }
+    if (on) {
+      T* dst = is_q ? static_cast<T*>(a.qo) + ((int64_t)token * a.qh + hh) * a.D
+                    : static_cast<T*>(a.ko) + ((int64_t)token * a.kh + hh) * a.D;
+      store8(dst + x0, v);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Cache write and read.
+// ---------------------------------------------------------------------------
+struct WriteArgs {
+  KvView w;
+  const void *k, *v;
+  int64_t k_ts, k_hs, v_ts, v_hs;
+};
+
+// Exponent of a row whose largest finite magnitude is amax (0 for a row of
+// zeros), held to a range in which 2^e, its inverse and every dequantised code
+// are normal numbers of fp32 and of bf16.
+__device__ __forceinline__ int kv_exponent(float amax) {
+  return max(-100, min(119, e4m3_row_exponent(amax)));
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+template <typename T, int LPR, bool F8>
+__device__ __forceinline__ void write_row(const T* src, void* pages, uint8_t* exps, int row, int D,
+                                          int x0) {
+  const bool on = row >= 0 && x0 < D;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (on) load8(src + x0, v);
+  if constexpr (F8) {
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float m = fabsf(v[j]);
+      amax = fmaxf(amax, m < INFINITY ? m : 0.f);     // NaN and infinities do not scale the row
+    }
+#pragma unroll
+    for (int m = LPR / 2; m; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+    const int e = kv_exponent(amax);
+    const float s = pow2(-e);
+    uint32_t c[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = fabsf(v[4 * j + i]) < INFINITY ? v[4 * j + i] * s : NAN;
+      c[j] = f32x2_to_e4m3(f[0], f[1]) | ((uint32_t)f32x2_to_e4m3(f[2], f[3]) << 16);
+    }
+    if (on) {
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pages) + (int64_t)row * D + x0) = make_uint2(c[0], c[1]);
+      if (x0 == 0) exps[row] = (uint8_t)(e + 127);
+    }
+  } else {
+    if (on) store8(static_cast<__nv_bfloat16*>(pages) + (int64_t)row * D + x0, v);
+  }
+}
+
+// A group of LPR lanes per (token, head): its key row and its value row.
+template <typename T, int LPR, bool F8>
+__global__ void __launch_bounds__(THREADS) k_cache_write(const __grid_constant__ WriteArgs a) {
+  const KvView& w = a.w;
+  const int64_t unit = ((int64_t)blockIdx.x * THREADS + threadIdx.x) / LPR;
+  const int token = (int)(unit / w.c.kv_heads), head = (int)(unit % w.c.kv_heads);
+  const int x0 = (threadIdx.x % LPR) * 8;
+  int row = -1;
+  if (unit < (int64_t)w.b.tokens * w.c.kv_heads) {
+    const int b = kv_sequence(w, token);
+    if (b >= 0)
+      row = kv_row(w, w.b.page_table + (int64_t)b * w.b.table_stride,
+                   (int64_t)__ldg(w.b.past + b) + (token - __ldg(w.b.first + b)), head);
+  }
+  write_row<T, LPR, F8>(static_cast<const T*>(a.k) + token * a.k_ts + head * a.k_hs, w.c.k, w.c.k_exp,
+                        row, w.c.head_dim, x0);
+  write_row<T, LPR, F8>(static_cast<const T*>(a.v) + token * a.v_ts + head * a.v_hs, w.c.v, w.c.v_exp,
+                        row, w.c.head_dim, x0);
+}
+
+struct ReadArgs {
+  KvView w;
+  void *k, *v;
+};
+
+template <typename T, bool F8>
+__device__ __forceinline__ void read_row(const void* pages, const uint8_t* exps, int row, int D, int x0,
+                                         T* dst) {
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (row >= 0) {
+    if constexpr (F8) {
+      const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pages) + (int64_t)row * D + x0);
+      // any byte is a power of two that fp32 holds, also in rows never written
+      const float s = pow2(max(-126, min(127, (int)exps[row] - 127)));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = e4m3_to_f32((uint8_t)((j < 4 ? c.x : c.y) >> (8 * (j & 3)))) * s;
+    } else {
+      load8(static_cast<const __nv_bfloat16*>(pages) + (int64_t)row * D + x0, v);
+    }
+  }
+  store8(dst + x0, v);
+}
+
+template <typename T, int LPR, bool F8>
+__global__ void __launch_bounds__(THREADS) k_cache_read(const __grid_constant__ ReadArgs a) {
+  const KvView& w = a.w;
+  const int64_t unit = ((int64_t)blockIdx.x * THREADS + threadIdx.x) / LPR;
+  const int token = (int)(unit / w.c.kv_heads), head = (int)(unit % w.c.kv_heads);
+  const int x0 = (threadIdx.x % LPR) * 8;
+  if (unit >= (int64_t)w.b.tokens * w.c.kv_heads || x0 >= w.c.head_dim) return;
+  const int b = kv_sequence(w, token);
+  if (b < 0) return;
+  const int row = kv_row(w, w.b.page_table + (int64_t)b * w.b.table_stride,
+                         (int64_t)__ldg(w.b.past + b) + (token - __ldg(w.b.first + b)), head);
+  const int64_t o = unit * w.c.head_dim;
+  read_row<T, F8>(w.c.k, w.c.k_exp, row, w.c.head_dim, x0, static_cast<T*>(a.k) + o);
+  read_row<T, F8>(w.c.v, w.c.v_exp, row, w.c.head_dim, x0, static_cast<T*>(a.v) + o);
+}
+
+// ---------------------------------------------------------------------------
+// Launches. The functors pick the template by type, lanes per row and format.
+// ---------------------------------------------------------------------------
+template <typename F> cudaError_t by_lanes(int D, F f) {
+  if (D <= 64) return f(std::integral_constant<int, 8>());
+  if (D <= 128) return f(std::integral_constant<int, 16>());
+  return f(std::integral_constant<int, 32>());
+}
+template <typename F> cudaError_t by_type(int dtype, F f) {
+  return dtype == DG_BF16 ? f(__nv_bfloat16()) : f(float());
+}
+
+// Blocks for n groups of lpr lanes; 0 if the grid would not fit.
+unsigned blocks(int64_t n, int lpr) {
+  const int64_t b = (n * lpr + THREADS - 1) / THREADS;
+  return b > 0x7fffffff ? 0u : (unsigned)b;
+}
+
+}  // namespace rows
+
+namespace {
+int fail(int code, const char* msg) {
+  set_last_error(msg);
+  return code;
+}
+bool off16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
+}  // namespace
+
+// Host checks of a cache and a batch, for the cache and attention calls; a
+// message in dg_last_error(NULL) and a code, or DG_OK.
+int kv_check(const dg_kv_cache* c, const dg_kv_batch* b) {
+  if (!c || !b) return fail(DG_EINVAL, "NULL cache or batch");
+  if (c->format != DG_KV_BF16 && c->format != DG_KV_E4M3) return fail(DG_EINVAL, "format must be DG_KV_BF16 or DG_KV_E4M3");
+  if (c->pages < 0 || c->page_size < 1 || c->kv_heads < 1) return fail(DG_EINVAL, "need pages >= 0, page_size >= 1, kv_heads >= 1");
+  if (c->head_dim < 16 || c->head_dim > 256 || c->head_dim % 16)
+    return fail(DG_EUNSUPPORTED, "head_dim must be a multiple of 16, 16..256");
+  // page_size and kv_heads < 2^31: their product and then the whole fit 64 and 96 bits
+  const int64_t per_page = (int64_t)c->page_size * c->kv_heads;
+  if (per_page >= (1ll << 31) || (c->pages && per_page > ((1ll << 31) - 1) / c->pages))
+    return fail(DG_EUNSUPPORTED, "the cache must have fewer than 2^31 rows (pages x kv_heads x page_size)");
+  if (b->batch < 0 || b->tokens < 0 || b->table_stride < 0) return fail(DG_EINVAL, "batch, tokens and table_stride must be >= 0");
+  if (b->batch > kMaxBatch) return fail(DG_EUNSUPPORTED, "batch must be at most 1024");
+  if ((int64_t)b->table_stride * c->page_size >= (1ll << 31))
+    return fail(DG_EUNSUPPORTED, "table_stride x page_size must be below 2^31");
+  if (b->batch == 0 || b->tokens == 0) return DG_OK;
+  if (!c->status || !b->first || !b->past) return fail(DG_EINVAL, "NULL status, first or past");
+  if (b->table_stride && !b->page_table) return fail(DG_EINVAL, "NULL page_table");
+  if (c->pages) {
+    if (!c->k || !c->v) return fail(DG_EINVAL, "NULL cache pages");
+    if (c->format == DG_KV_E4M3 && (!c->k_exp || !c->v_exp)) return fail(DG_EINVAL, "an e4m3 cache needs k_exp and v_exp");
+    if (off16(c->k) || off16(c->v)) return fail(DG_EINVAL, "cache pages must be 16-byte aligned");
+  }
+  return DG_OK;
+}
+
+int kv_row_args(const void* p, int64_t ts, int64_t hs) {
+  if (!p) return fail(DG_EINVAL, "NULL input");
+  if (off16(p) || ts % 8 || hs % 8) return fail(DG_EINVAL, "inputs must be 16-byte aligned, strides multiples of 8 elements");
+  return DG_OK;
+}
+
+int kv_launched(cudaError_t e) {
+  if (e == cudaSuccess) return DG_OK;
+  return fail(DG_ECUDA, cudaGetErrorString(e));
+}
+
+}  // namespace dg
+
+using namespace dg;
+
+extern "C" int dg_qk_norm_rope(int32_t tokens, int32_t q_heads, int32_t k_heads, int32_t head_dim,
+                               int32_t rot_dim, int32_t interleaved, int32_t dtype, const void* q,
+                               int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts, int64_t k_hs,
+                               const void* q_weight, const void* k_weight, float weight_offset,
+                               float eps, const int32_t* positions, const double* inv_freq,
+                               void* q_out, void* k_out, void* stream) {
+  using namespace rows;
+  if (tokens < 0 || q_heads < 0 || k_heads < 0) return fail(DG_EINVAL, "tokens and heads must be >= 0");
+  if (head_dim < 8 || head_dim > 256 || head_dim % 8) return fail(DG_EUNSUPPORTED, "head_dim must be a multiple of 8, 8..256");
+  if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16) return fail(DG_EUNSUPPORTED, "rot_dim must be a multiple of 16, 0..head_dim");
+  if (dtype != DG_F32 && dtype != DG_BF16) return fail(DG_EINVAL, "dtype must be DG_F32 or DG_BF16");
+  if (!(eps >= 0.f) || !std::isfinite(eps) || !std::isfinite(weight_offset)) return fail(DG_EINVAL, "need eps >= 0 and a finite weight_offset");
+  const int64_t heads = (int64_t)q_heads + k_heads;
+  if (tokens == 0 || heads == 0) return DG_OK;
+  if (heads > (1 << 20)) return fail(DG_EUNSUPPORTED, "too many heads");
+  int rc;
+  if (q_heads && (rc = kv_row_args(q, q_ts, q_hs))) return rc;
+  if (k_heads && (rc = kv_row_args(k, k_ts, k_hs))) return rc;
+  if ((q_heads && (!q_out || off16(q_out))) || (k_heads && (!k_out || off16(k_out))))
+    return fail(DG_EINVAL, "outputs must be 16-byte aligned and not NULL");
+  if (off16(q_weight) || off16(k_weight)) return fail(DG_EINVAL, "weights must be 16-byte aligned");
+  if (rot_dim && (!positions || !inv_freq)) return fail(DG_EINVAL, "a rotation needs positions and inv_freq");
+  NormArgs a{q, k, q_weight, k_weight, q_out, k_out, q_ts, q_hs, k_ts, k_hs, positions, inv_freq,
+             tokens, q_heads, k_heads, head_dim, rot_dim, 1, (int)heads, weight_offset, eps};
+  const cudaError_t e = by_lanes(head_dim, [&](auto lpr) {
+    constexpr int L = decltype(lpr)::value;
+    // As many heads per group as leave two full waves of threads, at most 8:
+    // they share the lane's sines and cosines.
+    const int64_t lanes = (int64_t)tokens * heads * L;
+    a.chunk = (int)std::min<int64_t>(std::min<int64_t>(8, heads), std::max<int64_t>(1, lanes / (148 * 2 * 2048)));
+    a.nchunk = (int)((heads + a.chunk - 1) / a.chunk);
+    const unsigned grid = blocks((int64_t)tokens * a.nchunk, L);
+    if (!grid) return cudaErrorInvalidConfiguration;
+    return by_type(dtype, [&](auto t) {
+      using T = decltype(t);
+      if (interleaved) k_norm_rope<T, L, true><<<grid, THREADS, 0, (cudaStream_t)stream>>>(a);
+      else k_norm_rope<T, L, false><<<grid, THREADS, 0, (cudaStream_t)stream>>>(a);
+      return cudaGetLastError();
+    });
+  });
+  return kv_launched(e);
+}
+
+extern "C" int dg_cache_write(const dg_kv_cache* cache, const dg_kv_batch* batch, int32_t dtype,
+                              const void* k, int64_t k_ts, int64_t k_hs, const void* v, int64_t v_ts,
+                              int64_t v_hs, void* stream) {
+  using namespace rows;
+  int rc = kv_check(cache, batch);
+  if (rc) return rc;
+  if (dtype != DG_F32 && dtype != DG_BF16) return fail(DG_EINVAL, "dtype must be DG_F32 or DG_BF16");
+  if (batch->tokens == 0 || batch->batch == 0) return DG_OK;
+  if ((rc = kv_row_args(k, k_ts, k_hs)) || (rc = kv_row_args(v, v_ts, v_hs))) return rc;
+  const WriteArgs a{{*cache, *batch}, k, v, k_ts, k_hs, v_ts, v_hs};
+  const int64_t n = (int64_t)batch->tokens * cache->kv_heads;
+  return kv_launched(by_lanes(cache->head_dim, [&](auto lpr) {
+    constexpr int L = decltype(lpr)::value;
+    const unsigned grid = blocks(n, L);
+    if (!grid) return cudaErrorInvalidConfiguration;
+    return by_type(dtype, [&](auto t) {
+      using T = decltype(t);
+      if (cache->format == DG_KV_E4M3) k_cache_write<T, L, true><<<grid, THREADS, 0, (cudaStream_t)stream>>>(a);
+      else k_cache_write<T, L, false><<<grid, THREADS, 0, (cudaStream_t)stream>>>(a);
+      return cudaGetLastError();
+    });
+  }));
+}
+
+extern "C" int dg_cache_read(const dg_kv_cache* cache, const dg_kv_batch* batch, int32_t dtype,
+                             void* k_out, void* v_out, void* stream) {
+  using namespace rows;
+  int rc = kv_check(cache, batch);
+  if (rc) return rc;
+  if (dtype != DG_F32 && dtype != DG_BF16) return fail(DG_EINVAL, "dtype must be DG_F32 or DG_BF16");
+  if (batch->tokens == 0 || batch->batch == 0) return DG_OK;
+  if (!k_out || !v_out || off16(k_out) || off16(v_out)) return fail(DG_EINVAL, "outputs must be 16-byte aligned and not NULL");
+  const ReadArgs a{{*cache, *batch}, k_out, v_out};
+  const int64_t n = (int64_t)batch->tokens * cache->kv_heads;
+  return kv_launched(by_lanes(cache->head_dim, [&](auto lpr) {
+    constexpr int L = decltype(lpr)::value;
+    const unsigned grid = blocks(n, L);
+    if (!grid) return cudaErrorInvalidConfiguration;
+    return by_type(dtype, [&](auto t) {
+      using T = decltype(t);
+      if (cache->format == DG_KV_E4M3) k_cache_read<T, L, true><<<grid, THREADS, 0, (cudaStream_t)stream>>>(a);
+      else k_cache_read<T, L, false><<<grid, THREADS, 0, (cudaStream_t)stream>>>(a);
+      return cudaGetLastError();
+    });
+  }));
+}
