@@ -5,11 +5,46 @@
 //   m = max t_j,  l = sum 2^(t_j - m),  out = sum 2^(t_j - m) v_j / l,
 //   lse = (m + log2 l) ln 2
 // in one pass over the keys: a larger maximum rescales l and the running sum.
+//
+// Rows. The query heads of one key/value head and the tokens of one sequence
+// are packed into one matrix, row r = token r / G, head r % G (G query heads
+// per key/value head), so that every key and value row is read once per
+// matrix and not once per query head. A tile has 128 such rows (the MMA's M,
+// one TMEM lane each); an item is NT tiles of one sequence and head.
+//
+// Work split. An item's keys come in tiles of BN. All items' key tiles, in
+// order (sequence, head, item), form one list, and CTA c of a persistent grid
+// takes a contiguous share of it: whatever the batch's lengths, every SM has
+// the same number of key tiles and there is one wave. A share may begin or end
+// inside an item; such pieces go to scratch with their m and l, and a second
+// launch joins them in the order of the list. Lengths are read on the device,
+// so a captured graph follows them.
+//
+// A CTA's warps:
+//   softmax   NT x 4 warps: TMEM lane = row; S from TMEM, P = 2^(t - m) back
+//             to TMEM as bf16, the running m and l in registers
+//   loads     SL warps, one per slot of the ring of key and value tiles: rows
+//             are gathered page by page (16-byte cp.async, or for e4m3 16-byte
+//             loads converted to bf16, which holds code x 2^e exactly) into
+//             the 128-byte swizzle that the MMA reads
+//   queries   one warp: the item's query rows
+//   MMA       one thread: S = Q K^T (both from shared memory), O += P V (P from
+//             TMEM, V as it lies, keys along K), accumulators in TMEM
+// With NT = 2 the two tiles share each key and value tile and alternate, so
+// that one tile's softmax runs under the other's products; with NT = 1 there
+// are two S buffers and S of the next tile is issued before P V of this one.
+//
+// O is rescaled only when a row's maximum has grown by more than 2^8 over the
+// one in use (P then stays below 2^8, harmless in bf16 and fp32): the wait for
+// the previous P V and the pass over O are rare.
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "dg.h"
 #include "dg_cache.cuh"
 #include "dg_fp8.cuh"
+#include "dg_tcgen05.cuh"
 
 namespace dg {
 void set_last_error(const char* msg);
@@ -19,76 +54,908 @@ int kv_launched(cudaError_t e);
 
 namespace attn {
 
+using namespace tc;
+
+constexpr int kMaxCtas = 148;                 // scratch is laid out for at most this many
+constexpr int TMEM_COLS = 512;
+constexpr float kGrow = 8.0f;                 // log2 growth of a maximum that rescales O
+constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr float kLn2 = 0.6931471805599453f;
+
 struct Args {
   KvView w;
   const __nv_bfloat16* q;
   int64_t q_ts, q_hs;
-  int q_heads;
+  int q_heads, G;
   float scale_log2;            // scale log2(e)
   int mask;
   const uint32_t* tree;
   int words;
   __nv_bfloat16* out;
   float* lse;
+  // scratch
+  float* part_o;               // [CTAs][2][rows][DP] unnormalised sums
+  float2* part_ml;             // [CTAs][2][rows] their m (log2 units) and l
+  struct Open* open;           // [CTAs] the item a CTA begins and does not finish
+  int rows;                    // rows kept per piece
 };
 
-// One warp per (token, query head), 8 elements of head_dim to a lane.
-template <bool F8>
-__global__ void __launch_bounds__(256) k_attend_rows(const __grid_constant__ Args a) {
-  const KvView& w = a.w;
-  const int64_t unit = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 32;
-  const int lane = threadIdx.x & 31;
-  if (unit >= (int64_t)w.b.tokens * a.q_heads) return;
-  const int token = (int)(unit / a.q_heads), h = (int)(unit % a.q_heads);
-  const int b = kv_sequence(w, token);
-  if (b < 0) return;
-  int t0;
-  const int n = kv_new(w, b, &t0);
-  const int i = token - t0, D = w.c.head_dim, kh = h / (a.q_heads / w.c.kv_heads);
-  const int64_t past = kv_past(w, b, n);
-  const int32_t* table = w.b.page_table + (int64_t)b * w.b.table_stride;
-  const int x0 = lane * 8;
-  float q[8] = {0, 0, 0, 0, 0, 0, 0, 0}, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (x0 < D)
-    for (int j = 0; j < 8; ++j) q[j] = to_f32(a.q[token * a.q_ts + h * a.q_hs + x0 + j]);
-  float m = -INFINITY, l = 0.f;
-  for (int64_t p = 0; p < past + n; ++p) {
-    if (p >= past) {
-      const int node = (int)(p - past);
-      if (a.mask == DG_MASK_CAUSAL && node > i) break;
-      if (a.mask == DG_MASK_TREE &&
-          (node / 32 >= a.words || !(a.tree[(int64_t)token * a.words + node / 32] >> (node % 32) & 1)))
-        continue;
+// The item that a CTA's share ends inside, if it also begins there.
+struct Open {
+  int on, b, h, m;
+  int64_t end;                 // of the item, in the list of key tiles
+  int64_t share;               // key tiles per CTA
+};
+
+template <int DP_, int NT_>
+struct Shape {
+  static constexpr int DP = DP_;                       // head_dim padded to 64, 128 or 256
+  static constexpr int NT = NT_;
+  static constexpr int BN = DP == 256 ? 64 : 128;      // keys per tile
+  static constexpr int SL = DP == 64 ? 6 : 4;          // ring slots (and load warps)
+  static constexpr int SLOT = BN * DP * 2;
+  static constexpr int QTILE = 128 * DP * 2;
+  static constexpr int W_LOAD = NT * 4, W_Q = W_LOAD + SL, W_MMA = W_Q + 1;
+  static constexpr int THREADS = (W_MMA + 1) * 32;
+  static constexpr int T_S = NT == 2 ? 128 : BN;       // TMEM columns between S buffers
+  static constexpr int T_O = NT == 2 ? 256 : 2 * BN;   // first column of O
+  static constexpr size_t SMEM = 1024 + (size_t)NT * QTILE + (size_t)SL * SLOT + 512 + 8 * (kMaxBatch + 1);
+  static_assert(T_O + NT * DP <= TMEM_COLS, "TMEM");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// ---------------------------------------------------------------------------
+// The list of key tiles.
+// ---------------------------------------------------------------------------
+template <int ROWS, int BN>
+struct Walk {
+  const Args& a;
+  int b, h, m;                 // sequence, key/value head, item of the pair
+  int n, past, t0;             // the sequence's new tokens, cached positions, first row
+  int tb, te, T;               // this segment's key tiles [tb, te) of the item's T
+  int64_t pos, hi;             // position in the list, end of the CTA's share
+
+  __device__ __forceinline__ Walk(const Args& a_) : a(a_) {}
+  __device__ __forceinline__ void sequence(int b_) {
+    b = b_;
+    n = kv_new(a.w, b, &t0);
+    past = kv_past(a.w, b, n);
+  }
+  __device__ __forceinline__ int items() const { return (int)(((int64_t)n * a.G + ROWS - 1) / ROWS); }
+  // Key tiles of item x: up to its last row's token under a causal mask, else all; at least one.
+  __device__ __forceinline__ int tiles(int x) const {
+    int64_t e = n;
+    if (a.mask == DG_MASK_CAUSAL) {
+      const int64_t upto = ((int64_t)(x + 1) * ROWS + a.G - 1) / a.G;
+      e = upto < e ? upto : e;
     }
-    const int row = kv_row(w, table, p, kh);
-    float k[8] = {0, 0, 0, 0, 0, 0, 0, 0}, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (row >= 0 && x0 < D) {
-      const int64_t at = (int64_t)row * D + x0;
-      for (int j = 0; j < 8; ++j) {
-        if (F8) {
-          k[j] = ldexpf(e4m3_to_f32(static_cast<const uint8_t*>(w.c.k)[at + j]), w.c.k_exp[row] - 127);
-          v[j] = ldexpf(e4m3_to_f32(static_cast<const uint8_t*>(w.c.v)[at + j]), w.c.v_exp[row] - 127);
-        } else {
-          k[j] = to_f32(static_cast<const __nv_bfloat16*>(w.c.k)[at + j]);
-          v[j] = to_f32(static_cast<const __nv_bfloat16*>(w.c.v)[at + j]);
-        }
+    const int64_t t = ((int64_t)past + e + BN - 1) / BN;
+    return t < 1 ? 1 : (int)t;
+  }
+  __device__ __forceinline__ int64_t keys() const { return (int64_t)past + n; }
+  // First position that some row of the item may not see.
+  __device__ __forceinline__ int64_t clear() const {
+    return a.mask == DG_MASK_FULL ? keys() : a.mask == DG_MASK_TREE ? past : past + (int64_t)m * ROWS / a.G + 1;
+  }
+  __device__ __forceinline__ bool more() const { return pos < hi; }
+  __device__ __forceinline__ void next() {
+    pos += te - tb;
+    if (pos >= hi) return;
+    if (++m == items()) {
+      m = 0;
+      if (++h == a.w.c.kv_heads) {
+        h = 0;
+        do { sequence(b + 1); } while (n == 0);       // the list ends before the batch does
       }
     }
-    float s = 0.f;
-    for (int j = 0; j < 8; ++j) s = fmaf(q[j], k[j], s);
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    const float t = s * a.scale_log2;
-    const float mn = fmaxf(m, t);
-    const float c = exp2f(m - mn), e = exp2f(t - mn);
-    m = mn;
-    l = l * c + e;
-    for (int j = 0; j < 8; ++j) o[j] = fmaf(e, v[j], o[j] * c);
+    T = tiles(m);
+    tb = 0;
+    te = (int)(T < hi - pos ? T : hi - pos);
   }
-  const float r = l > 0.f ? 1.f / l : 0.f;
-  if (x0 < D)
-    for (int j = 0; j < 8; ++j)
-      a.out[unit * D + x0 + j] = __float2bfloat16_rn(l == l ? o[j] * r : l);
-  if (a.lse && lane == 0) a.lse[unit] = (m + log2f(l)) * 0.6931471805599453f;
+  __device__ __forceinline__ int rows() const {
+    const int64_t r = (int64_t)n * a.G - (int64_t)m * ROWS;
+    return r < ROWS ? (int)r : ROWS;
+  }
+};
+
+// Where a CTA's share begins; worked out once per CTA.
+struct Start {
+  int64_t lo, hi, share;
+  int b, h, m, tb;
+};
+
+// The whole CTA: tiles per head of every sequence, their prefix sums (in
+// shared memory, pref[batch + 1]), and this CTA's share.
+template <int ROWS, int BN>
+__device__ __forceinline__ void plan(const Args& a, int64_t* pref, Start* st) {
+  const int B = a.w.b.batch;
+  Walk<ROWS, BN> w(a);
+  constexpr int kAlone = 16;                          // items that one thread adds up by itself
+  for (int b = threadIdx.x; b < B; b += blockDim.x) {
+    w.sequence(b);
+    const int it = w.items();
+    int64_t u = 0;
+    if (a.mask != DG_MASK_CAUSAL) u = it ? (int64_t)it * w.tiles(0) : 0;
+    else if (it > kAlone) u = -1;
+    else for (int x = 0; x < it; ++x) u += w.tiles(x);
+    pref[b + 1] = u;
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int b = warp; b < B; b += blockDim.x >> 5) {
+    if (pref[b + 1] >= 0) continue;
+    w.sequence(b);
+    int64_t u = 0;
+    for (int x = lane, it = w.items(); x < it; x += 32) u += w.tiles(x);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
+    __syncwarp();
+    if (lane == 0) pref[b + 1] = u;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int64_t run = 0;
+    if (lane == 0) pref[0] = 0;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      int64_t u = b0 + lane < B ? pref[b0 + lane + 1] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, u, d);
+        if (lane >= d) u += o;
+      }
+      if (b0 + lane < B) pref[b0 + lane + 1] = run + u;
+      run += __shfl_sync(0xffffffffu, u, 31);
+    }
+    __syncwarp();
+    if (lane == 0) {
+      const int H = a.w.c.kv_heads;
+      const int64_t total = run * H;
+      const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+      st->share = share;
+      st->lo = min(total, share * (int64_t)blockIdx.x);
+      st->hi = min(total, st->lo + share);
+      if (st->lo < st->hi) {
+        int l = 0, r = B;                             // H pref[l] <= lo < H pref[r]
+        while (r - l > 1) {
+          const int mid = (l + r) >> 1;
+          if (pref[mid] * H <= st->lo) l = mid;
+          else r = mid;
+        }
+        w.sequence(l);
+        const int64_t per = pref[l + 1] - pref[l];
+        int64_t rest = st->lo - pref[l] * H;
+        st->b = l;
+        st->h = (int)(rest / per);
+        rest -= st->h * per;
+        int x = 0;
+        if (a.mask != DG_MASK_CAUSAL) {
+          x = (int)(rest / w.tiles(0));
+          rest -= (int64_t)x * w.tiles(0);
+        } else {
+          for (int t; rest >= (t = w.tiles(x)); ++x) rest -= t;
+        }
+        st->m = x;
+        st->tb = (int)rest;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+template <int ROWS, int BN>
+__device__ __forceinline__ void begin(Walk<ROWS, BN>& w, const Start& st) {
+  w.pos = st.lo;
+  w.hi = st.hi;
+  if (w.pos >= w.hi) return;
+  w.sequence(st.b);
+  w.h = st.h;
+  w.m = st.m;
+  w.T = w.tiles(w.m);
+  w.tb = st.tb;
+  w.te = (int)(w.T - w.tb < w.hi - w.pos ? w.T : w.tb + (w.hi - w.pos));
+}
+
+// ---------------------------------------------------------------------------
+// Small pieces.
+// ---------------------------------------------------------------------------
+struct Sync {
+  uint64_t full[8], empty[8];      // ring slots
+  uint64_t s_full[2], p_full[2];   // S ready; P stored
+  uint64_t o_done[2], o_free[2];   // P V done; O read
+  uint64_t q_full, q_free, fin;
+  uint32_t tmem;
+  int abort, nonfinite;
+  Start start;
+};
+
+// Bounded wait on an mbarrier phase; gives up on the CTA's abort flag or after
+// kWaitNs (then raises DG_ETIMEOUT). check_abort = false: time limit only.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_s,
+                                       int* status, bool check_abort) {
+  const uint64_t t0 = gtimer();
+  for (uint32_t k = 1;; ++k) {
+    if (mbar_try(bar, parity)) return true;
+    if ((k & 63) == 0) {
+      if (check_abort && *abort_s) return false;
+      if (gtimer() - t0 > kWaitNs) {
+        *abort_s = 1;
+        raise_status(status, DG_ETIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Sync& sy, const Args& a,
+                                     bool check_abort = true) {
+  return mbar_try(bar, parity) || wait_slow(bar, parity, &sy.abort, a.w.c.status, check_abort);
+}
+
+// D (TMEM) += A (TMEM, bf16) B (shared memory).
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 16 registers of each lane to 16 columns of TMEM.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// 16 bytes into shared memory, or zeros where `bytes` is 0.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void st_shared(uint32_t dst, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(src) : "memory");
+  return v;
+}
+// Byte offset of 16-byte chunk c (8 bf16 columns) of row r in an operand tile of
+// `rows` rows: blocks of 64 columns, 128-byte rows, the chunk index xored with r % 8.
+__device__ __forceinline__ uint32_t swizzled(int r, int c, int rows) {
+  return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+// The lowest k bits (none for k <= 0, all for k >= 32).
+__device__ __forceinline__ uint32_t low_bits(int64_t k) {
+  return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << (int)k) - 1u;
+}
+// 32 bits of a bit row from bit `at` on (may be negative); words beyond the row are zero.
+__device__ __forceinline__ uint32_t bits_at(const uint32_t* row, int words, int64_t at) {
+  if (at <= -32 || at >= (int64_t)words * 32) return 0;
+  const int64_t x = at >= 0 ? at >> 5 : -1;
+  const uint32_t lo = x >= 0 ? __ldg(row + x) : 0u;
+  const uint32_t hi = x + 1 < words ? __ldg(row + x + 1) : 0u;
+  return __funnelshift_r(lo, hi, (uint32_t)(at & 31));
+}
+// Which of 32 positions from `at` on token i of the sequence sees.
+template <typename W>
+__device__ __forceinline__ uint32_t seen(const W& w, const uint32_t* tree, int i, int64_t at) {
+  if (w.a.mask == DG_MASK_CAUSAL) return low_bits((int64_t)w.past + i + 1 - at);
+  const uint32_t in = low_bits(w.keys() - at);
+  if (w.a.mask == DG_MASK_FULL) return in;
+  return in & (low_bits(w.past - at) | bits_at(tree, w.a.words, at - w.past));
+}
+__device__ __forceinline__ bool finite_bf16(uint32_t half) { return (half & 0x7f80u) != 0x7f80u; }
+// A pair of bf16 with what is not finite replaced by zero.
+__device__ __forceinline__ uint32_t only_finite(uint32_t x) {
+  if (!finite_bf16(x)) x &= 0xffff0000u;
+  if (!finite_bf16(x >> 16)) x &= 0x0000ffffu;
+  return x;
+}
+
+// ---------------------------------------------------------------------------
+// Loads.
+// ---------------------------------------------------------------------------
+// Two e4m3 codes to bf16 x 2^e; exact (4 significant bits, and the exponents
+// of a written cache keep code and product normal).
+__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t pair, float scale) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)pair));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack_bf16(f.x * scale, f.y * scale);
+}
+
+// One warp fills one ring slot with the BN key (or value) rows from position
+// j0 on. `clean`: rows that a query row of the item may not see hold values
+// that must not reach it; what is not finite is then replaced by zero and
+// noted (0 x NaN in the second product would reach every row).
+template <class S, bool F8, typename W>
+__device__ __forceinline__ void load_rows(const W& w, const void* pages, const uint8_t* exps, int64_t j0,
+                                          uint32_t dst, bool clean, Sync& sy) {
+  constexpr int PER = S::BN / 32;
+  const Args& a = w.a;
+  const int lane = threadIdx.x & 31;
+  const int D = a.w.c.head_dim;
+  const int32_t* table = a.w.b.page_table + (int64_t)w.b * a.w.b.table_stride;
+  const int64_t L = w.keys();
+  int row[PER];                                    // rows lane, lane + 32, ...: cache row or -1
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    const int64_t j = j0 + p * 32 + lane;
+    row[p] = j < L ? kv_row(a.w, table, j, w.h) : -1;
+  }
+  if constexpr (!F8) {
+    constexpr int CPR = S::DP / 8, RPI = 32 / CPR; // chunks per row, rows per instruction
+    const int c = lane % CPR;
+    const bool in = c * 8 < D;
+    const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(pages) + c * 8;
+#pragma unroll
+    for (int it = 0; it < S::BN / RPI; ++it) {
+      const int r = it * RPI + lane / CPR;
+      const int cr = __shfl_sync(0xffffffffu, row[it * RPI / 32], r & 31);
+      const bool on = in && cr >= 0;
+      copy16(dst + swizzled(r, c, S::BN), on ? base + (int64_t)cr * D : a.q, on ? 16 : 0);
+    }
+    copies_landed();
+    if (clean) {
+      bool dirty = false;
+      for (int it = 0; it < S::BN / RPI; ++it) {
+        const uint32_t at = dst + swizzled(it * RPI + lane / CPR, c, S::BN);
+        const uint4 v = ld_shared(at);
+        const uint4 f = make_uint4(only_finite(v.x), only_finite(v.y), only_finite(v.z), only_finite(v.w));
+        if (f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w) {
+          st_shared(at, f);
+          dirty = true;
+        }
+      }
+      if (dirty) *(volatile int*)&sy.nonfinite = 1;
+    }
+  } else {
+    constexpr int CPR = S::DP / 16, RPI = 32 / CPR, N = S::BN / RPI, BATCH = 8;
+    const int c = lane % CPR;
+    const bool in = c * 16 < D;
+    const uint8_t* base = static_cast<const uint8_t*>(pages) + c * 16;
+    float scale[PER];
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+      scale[p] = row[p] >= 0 ? __uint_as_float(max(1u, min(254u, (uint32_t)__ldg(exps + row[p]))) << 23) : 0.f;
+#pragma unroll
+    for (int i0 = 0; i0 < N; i0 += BATCH) {
+      uint4 v[BATCH];
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const int r = (i0 + k) * RPI + lane / CPR;
+        const int cr = __shfl_sync(0xffffffffu, row[(i0 + k) * RPI / 32], r & 31);
+        v[k] = make_uint4(0, 0, 0, 0);
+        if (in && cr >= 0) v[k] = __ldg(reinterpret_cast<const uint4*>(base + (int64_t)cr * D));
+      }
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const int r = (i0 + k) * RPI + lane / CPR;
+        const float s = __shfl_sync(0xffffffffu, scale[(i0 + k) * RPI / 32], r & 31);
+        const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          o[2 * t] = codes_to_bf16(x[t], s);
+          o[2 * t + 1] = codes_to_bf16(x[t] >> 16, s);
+        }
+        if (clean) {
+          bool dirty = false;
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            const uint32_t f = only_finite(o[t]);
+            dirty |= f != o[t];
+            o[t] = f;
+          }
+          if (dirty) *(volatile int*)&sy.nonfinite = 1;
+        }
+        st_shared(dst + swizzled(r, 2 * c, S::BN), make_uint4(o[0], o[1], o[2], o[3]));
+        st_shared(dst + swizzled(r, 2 * c + 1, S::BN), make_uint4(o[4], o[5], o[6], o[7]));
+      }
+    }
+  }
+}
+
+// What load_rows left out of value columns d .. d + 7 of a cache row: its
+// infinities and NaN, zero elsewhere.
+template <bool F8>
+__device__ __forceinline__ void not_finite8(const Args& a, int row, int d, float* v) {
+  const int64_t at = (int64_t)row * a.w.c.head_dim + d;
+  if constexpr (F8) {
+    const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.w.c.v) + at);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t code = (j < 4 ? c.x : c.y) >> (8 * (j & 3));
+      v[j] = (code & 0x7f) == 0x7f ? NAN : 0.f;
+    }
+  } else {
+    const uint4 c = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.w.c.v) + at);
+    const uint32_t x[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t half = x[j >> 1] >> (16 * (j & 1)) & 0xffffu;
+      v[j] = finite_bf16(half) ? 0.f : __uint_as_float(half << 16);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The kernel.
+// ---------------------------------------------------------------------------
+template <class S, bool F8>
+__global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant__ Args a) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* ring = smem + S::NT * S::QTILE;
+  Sync& sy = *reinterpret_cast<Sync*>(ring + S::SL * S::SLOT);
+  static_assert(sizeof(Sync) <= 512, "barriers");
+  int64_t* pref = reinterpret_cast<int64_t*>(ring + S::SL * S::SLOT + 512);
+  constexpr int ROWS = S::NT * 128, BN = S::BN;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::SL; ++s) { mbar_init(&sy.full[s], 1); mbar_init(&sy.empty[s], 1); }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&sy.s_full[x], 1);
+      mbar_init(&sy.p_full[x], 4);
+      mbar_init(&sy.o_done[x], 1);
+      mbar_init(&sy.o_free[x], 4);
+    }
+    mbar_init(&sy.q_full, 1);
+    mbar_init(&sy.q_free, 1);
+    mbar_init(&sy.fin, 1);
+    sy.abort = 0;
+    sy.nonfinite = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == S::W_MMA) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::
+                     "r"(smem_u32(&sy.tmem)), "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  plan<ROWS, BN>(a, pref, &sy.start);                 // ends with a block barrier
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tmem = *(volatile uint32_t*)&sy.tmem;
+  Walk<ROWS, BN> w(a);
+  begin(w, sy.start);
+
+  if (warp < S::W_LOAD) {
+    // ---------------------------------------------------------------- softmax
+    const int x = warp >> 2;                          // row tile
+    const int quarter = warp & 3;
+    const int r = x * 128 + quarter * 32 + lane;      // row within the item
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t t_o = tmem + S::T_O + x * S::DP + lanes;
+    bool ok = true;
+    uint32_t gt = 0;                                  // key tiles done by this CTA
+    int open_b = -1, open_h = 0, open_m = 0;          // an item begun and not finished
+    int64_t open_end = 0;
+    for (; w.more() && ok; w.next()) {
+      const int rows = w.rows();
+      const bool any = x * 128 + quarter * 32 < rows; // warp-uniform
+      const bool valid = r < rows;
+      const int64_t rid = (int64_t)w.m * ROWS + (valid ? r : 0);
+      const int i = (int)(rid / a.G), g = (int)(rid - (int64_t)i * a.G);
+      const uint32_t* tree = a.mask == DG_MASK_TREE ? a.tree + (int64_t)(w.t0 + i) * a.words : nullptr;
+      // tiles that reach beyond this position hold some that the row may not see
+      const int64_t clear = a.mask == DG_MASK_FULL ? w.keys() : a.mask == DG_MASK_CAUSAL ? (int64_t)w.past + i + 1 : w.past;
+      float m = -INFINITY, l = 0.f;                   // m in log2 units
+      for (int t = w.tb; t < w.te; ++t, ++gt) {
+        const int buf = S::NT == 2 ? x : (int)(gt & 1);
+        const uint32_t ph = S::NT == 2 ? gt & 1 : (gt >> 1) & 1;
+        if (!__all_sync(0xffffffffu, wait(&sy.s_full[buf], ph, sy, a))) { ok = false; break; }
+        if (any) {
+          tc_fence_after();
+          const uint32_t t_s = tmem + buf * S::T_S + lanes;
+          const int64_t j0 = (int64_t)t * BN;
+          const bool masked = __any_sync(0xffffffffu, j0 + BN > clear);
+          uint32_t word[BN / 32];
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) word[c] = masked ? seen(w, tree, i, j0 + c * 32) : 0xffffffffu;
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) {
+            float s[32];
+            tmem_ld32(t_s + c * 32, s);
+            if (masked) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) s[j] = (word[c] >> j) & 1 ? s[j] : -INFINITY;
+            }
+            float u0 = -INFINITY, u1 = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              u0 = fmaxf(u0, fmaxf(s[j], s[j + 1]));
+              u1 = fmaxf(u1, fmaxf(s[j + 2], s[j + 3]));
+            }
+            top = fmaxf(top, fmaxf(u0, u1));
+          }
+          top *= a.scale_log2;
+          // the maximum in use moves at the first tile and when it has grown by kGrow
+          const bool first = t == w.tb;
+          const bool move = top > m + kGrow || (m == -INFINITY && top > m);
+          if (!first && __any_sync(0xffffffffu, move && valid)) {
+            if (!__all_sync(0xffffffffu, wait(&sy.o_done[x], (gt - 1) & 1, sy, a))) { ok = false; break; }
+            tc_fence_after();
+            const float f = move ? ex2(m - top) : 1.f;
+            l *= f;
+#pragma unroll 1
+            for (int c = 0; c < S::DP / 32; ++c) {
+              float o[32];
+              tmem_ld32(t_o + c * 32, o);
+              uint32_t p[32];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) p[j] = __float_as_uint(o[j] * f);
+              tmem_st16(t_o + c * 32, p);
+              tmem_st16(t_o + c * 32 + 16, p + 16);
+            }
+            tmem_st_wait();
+          }
+          if (move) m = top;
+          const float sub = m == -INFINITY ? 0.f : m;  // a row that has seen nothing yet: P = 0
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) {
+            float s[32];
+            tmem_ld32(t_s + c * 32, s);
+            if (masked) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) s[j] = (word[c] >> j) & 1 ? s[j] : -INFINITY;
+            }
+            uint32_t p[16];
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float e0 = ex2(fmaf(s[j], a.scale_log2, -sub));
+              const float e1 = ex2(fmaf(s[j + 1], a.scale_log2, -sub));
+              l0 += e0;
+              l1 += e1;
+              p[j >> 1] = pack_bf16(e0, e1);
+            }
+            tmem_st16(t_s + c * 16, p);
+          }
+          l += l0 + l1;
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sy.p_full[buf]);
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- the segment's result
+      if (!__all_sync(0xffffffffu, wait(&sy.o_done[x], (gt - 1) & 1, sy, a))) { ok = false; break; }
+      const bool whole = w.tb == 0 && w.te == w.T;
+      const bool fix = a.mask != DG_MASK_FULL && *(volatile int*)&sy.nonfinite;
+      const int piece = blockIdx.x * 2 + (w.tb == 0 ? 1 : 0);
+      if (any) {
+        tc_fence_after();
+        const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+        const int64_t orow = (int64_t)(w.t0 + i) * a.q_heads + w.h * a.G + g;
+#pragma unroll 1
+        for (int c = 0; c < S::DP / 32; ++c) {
+          float o[32];
+          tmem_ld32(t_o + c * 32, o);
+          if (fix && valid) {
+            // what load_rows left out, for the rows that do see it
+            const int64_t k1 = min(w.keys(), (int64_t)w.te * BN);
+            for (int64_t j = max(w.clear() / BN * BN, (int64_t)w.tb * BN); j < k1; ++j) {
+              if (!(seen(w, tree, i, j) & 1)) continue;
+              const int row = kv_row(a.w, a.w.b.page_table + (int64_t)w.b * a.w.b.table_stride, j, w.h);
+              if (row < 0) continue;
+#pragma unroll
+              for (int d = 0; d < 32; d += 8) {
+                if (c * 32 + d >= a.w.c.head_dim) break;
+                float v[8];
+                not_finite8<F8>(a, row, c * 32 + d, v);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[d + k] += v[k];
+              }
+            }
+          }
+          if (!valid) continue;
+          if (whole) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (c * 32 + k * 8 >= a.w.c.head_dim) break;
+              uint4 v;
+              v.x = pack_bf16(o[8 * k] * inv, o[8 * k + 1] * inv);
+              v.y = pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv);
+              v.z = pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv);
+              v.w = pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv);
+              *reinterpret_cast<uint4*>(a.out + orow * a.w.c.head_dim + c * 32 + k * 8) = v;
+            }
+          } else {
+            float* dst = a.part_o + ((int64_t)piece * a.rows + r) * S::DP + c * 32;
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4*>(dst + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          }
+        }
+        if (valid && whole && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        if (valid && !whole) a.part_ml[(int64_t)piece * a.rows + r] = make_float2(m, l);
+        tc_fence_before();
+      }
+      if (w.tb == 0 && w.te < w.T) {
+        open_b = w.b;
+        open_h = w.h;
+        open_m = w.m;
+        open_end = w.pos + w.T;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sy.o_free[x]);
+    }
+    if (threadIdx.x == 0)
+      a.open[blockIdx.x] = Open{ok && open_b >= 0, open_b, open_h, open_m, open_end, sy.start.share};
+  } else if (warp < S::W_Q) {
+    // ---------------------------------------------------------------- key and value loads
+    const int slot = warp - S::W_LOAD;
+    const uint32_t dst = smem_u32(ring + slot * S::SLOT);
+    bool ok = true;
+    uint32_t e = 0, uses = 0;                         // ring entries so far; those of this slot
+    for (; w.more() && ok; w.next()) {
+      for (int t = w.tb; t < w.te && ok; ++t)
+        for (int kv = 0; kv < 2; ++kv, ++e) {
+          if ((int)(e % S::SL) != slot) continue;
+          if (!__all_sync(0xffffffffu, wait(&sy.empty[slot], (uses & 1) ^ 1, sy, a))) { ok = false; break; }
+          ++uses;
+          const int64_t j0 = (int64_t)t * BN;
+          const bool clean = kv && a.mask != DG_MASK_FULL && j0 + BN > w.clear();
+          load_rows<S, F8>(w, kv ? a.w.c.v : a.w.c.k, kv ? a.w.c.v_exp : a.w.c.k_exp, j0, dst, clean, sy);
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sy.full[slot]);
+        }
+    }
+  } else if (warp == S::W_Q) {
+    // ---------------------------------------------------------------- queries
+    bool ok = true;
+    uint32_t seg = 0;
+    const int D = a.w.c.head_dim;
+    for (; w.more() && ok; w.next(), ++seg) {
+      if (seg && !__all_sync(0xffffffffu, wait(&sy.q_free, (seg - 1) & 1, sy, a))) { ok = false; break; }
+      constexpr int CPR = S::DP / 8, RPI = 32 / CPR;
+      const int c = lane % CPR;
+      const int rows = w.rows();
+      const uint32_t dst = smem_u32(smem);
+      for (int r0 = 0; r0 < rows; r0 += RPI) {
+        const int r = r0 + lane / CPR;
+        const int64_t rid = (int64_t)w.m * ROWS + (r < rows ? r : 0);
+        const int64_t i = rid / a.G, g = rid - i * a.G;
+        const bool on = r < rows && c * 8 < D;
+        copy16(dst + (r >> 7) * S::QTILE + swizzled(r & 127, c, 128),
+               on ? a.q + (w.t0 + i) * a.q_ts + (w.h * a.G + g) * a.q_hs + c * 8 : a.q, on ? 16 : 0);
+      }
+      copies_landed();
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sy.q_full);
+    }
+  } else {
+    // ---------------------------------------------------------------- MMA
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_bf16(128, BN, 0), id_o = idesc_bf16(128, S::DP, 1);
+      const uint32_t q0 = smem_u32(smem), ring0 = smem_u32(ring);
+      uint32_t e = 0, gt = 0, seg = 0;                // ring entries, key tiles and segments so far
+      bool ok = true;
+      auto slot_full = [&](uint32_t entry) {
+        if (!wait(&sy.full[entry % S::SL], (entry / S::SL) & 1, sy, a)) return false;
+        tc_fence_after();
+        return true;
+      };
+      auto scores = [&](uint32_t entry, int x, int buf) {   // S(buf) = Q(x) K^T
+        const uint32_t k0 = ring0 + (entry % S::SL) * S::SLOT;
+#pragma unroll
+        for (int k = 0; k < S::DP / 16; ++k)
+          mma_bf16(tmem + buf * S::T_S,
+                   sdesc(q0 + x * S::QTILE + (k >> 2) * (128 * 128) + (k & 3) * 32, 16, 1024),
+                   sdesc(k0 + (k >> 2) * (BN * 128) + (k & 3) * 32, 16, 1024), id_s, k ? 1u : 0u);
+        mma_commit(&sy.s_full[buf]);
+      };
+      auto sums = [&](uint32_t entry, int x, int buf, bool first) {   // O(x) += P(buf) V
+        const uint32_t v0 = ring0 + (entry % S::SL) * S::SLOT;
+#pragma unroll
+        for (int k = 0; k < BN / 16; ++k)
+          mma_bf16_ts(tmem + S::T_O + x * S::DP, tmem + buf * S::T_S + k * 8,
+                      sdesc(v0 + k * 2048, BN * 128, 1024), id_o, first && k == 0 ? 0u : 1u);
+        mma_commit(&sy.o_done[x]);
+      };
+      for (; w.more() && ok; w.next(), ++seg) {
+        if (!wait(&sy.q_full, seg & 1, sy, a) || !slot_full(e)) { ok = false; break; }
+        const int n = w.te - w.tb;
+        if constexpr (S::NT == 2) {
+          scores(e, 0, 0);
+          scores(e, 1, 1);
+          mma_commit(&sy.empty[e % S::SL]);
+          if (n == 1) mma_commit(&sy.q_free);
+          for (int t = 0; t < n && ok; ++t, ++gt, e += 2) {
+            for (int x = 0; x < 2; ++x) {
+              if (!wait(&sy.p_full[x], gt & 1, sy, a) ||
+                  (t == 0 && seg && !wait(&sy.o_free[x], (seg - 1) & 1, sy, a)) ||
+                  (x == 0 && !slot_full(e + 1))) { ok = false; break; }
+              tc_fence_after();
+              sums(e + 1, x, x, t == 0);
+              if (x == 1) mma_commit(&sy.empty[(e + 1) % S::SL]);
+              if (t + 1 < n) {
+                if (x == 0 && !slot_full(e + 2)) { ok = false; break; }
+                scores(e + 2, x, x);
+                if (x == 1) {
+                  mma_commit(&sy.empty[(e + 2) % S::SL]);
+                  if (t + 2 == n) mma_commit(&sy.q_free);
+                }
+              }
+            }
+          }
+        } else {
+          scores(e, 0, gt & 1);
+          mma_commit(&sy.empty[e % S::SL]);
+          if (n == 1) mma_commit(&sy.q_free);
+          for (int t = 0; t < n && ok; ++t, ++gt, e += 2) {
+            if (t + 1 < n) {
+              if (!slot_full(e + 2)) { ok = false; break; }
+              scores(e + 2, 0, (gt + 1) & 1);
+              mma_commit(&sy.empty[(e + 2) % S::SL]);
+              if (t + 2 == n) mma_commit(&sy.q_free);
+            }
+            if (!wait(&sy.p_full[gt & 1], (gt >> 1) & 1, sy, a) ||
+                (t == 0 && seg && !wait(&sy.o_free[0], (seg - 1) & 1, sy, a)) || !slot_full(e + 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            sums(e + 1, 0, gt & 1, t == 0);
+            mma_commit(&sy.empty[(e + 1) % S::SL]);
+          }
+        }
+      }
+      // every MMA issued has completed before TMEM is released and the CTA exits
+      mma_commit(&sy.fin);
+      wait(&sy.fin, 0, sy, a, false);
+    }
+    __syncwarp();
+  }
+  copies_landed();
+  __syncthreads();
+  if (warp == S::W_MMA) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS)
+                 : "memory");
+  }
+}
+
+// Joins the pieces of the items that lie in more than one CTA's share: block
+// (c, y) those rows y, y + gridDim.y, ... of the item that CTA c began. Pieces
+// are added in the order of their keys by groups of warps, so that the result
+// does not depend on timing.
+template <class S>
+__global__ void __launch_bounds__(256) k_join(const __grid_constant__ Args a) {
+  constexpr int V = S::DP / 32;                       // columns per lane
+  __shared__ float o_s[8][S::DP];
+  __shared__ float m_s[8], l_s[8];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Open op = a.open[blockIdx.x];
+  if (!op.on) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Walk<S::NT * 128, S::BN> w(a);
+  w.sequence(op.b);
+  w.h = op.h;
+  w.m = op.m;
+  const int rows = w.rows(), D = a.w.c.head_dim;
+  const int pieces = (int)((op.end - 1) / op.share) - (int)blockIdx.x + 1;
+  const int per = pieces > 4 ? 8 : pieces > 2 ? 4 : 2;   // warps per row
+  const int sub = warp % per;
+  for (int r0 = blockIdx.y * (8 / per); r0 < rows; r0 += gridDim.y * (8 / per)) {
+    const int r = r0 + warp / per;
+    float m = -INFINITY, l = 0.f, o[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] = 0.f;
+    if (r < rows) {
+#pragma unroll 4
+      for (int p = sub; p < pieces; p += per) {
+        const int64_t at = (int64_t)((blockIdx.x + p) * 2 + (p == 0 ? 1 : 0)) * a.rows + r;
+        const float2 ml = a.part_ml[at];
+        const float* src = a.part_o + at * S::DP + lane * V;
+        float v[V];
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+          const float2 f = *reinterpret_cast<const float2*>(src + k);
+          v[k] = f.x;
+          v[k + 1] = f.y;
+        }
+        const float mn = fmaxf(m, ml.x);
+        const float sub_m = mn == -INFINITY ? 0.f : mn;
+        const float f0 = ex2(m - sub_m), f1 = ex2(ml.x - sub_m);
+        l = l * f0 + ml.y * f1;
+#pragma unroll
+        for (int k = 0; k < V; ++k) o[k] = o[k] * f0 + v[k] * f1;
+        m = mn;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) o_s[warp][lane * V + k] = o[k];
+    if (lane == 0) { m_s[warp] = m; l_s[warp] = l; }
+    __syncthreads();
+    if (sub == 0 && r < rows) {
+      for (int p = 1; p < per; ++p) {
+        const float pm = m_s[warp + p], pl = l_s[warp + p];
+        const float mn = fmaxf(m, pm);
+        const float sub_m = mn == -INFINITY ? 0.f : mn;
+        const float f0 = ex2(m - sub_m), f1 = ex2(pm - sub_m);
+        l = l * f0 + pl * f1;
+#pragma unroll
+        for (int k = 0; k < V; ++k) o[k] = o[k] * f0 + o_s[warp + p][lane * V + k] * f1;
+        m = mn;
+      }
+      const int64_t rid = (int64_t)w.m * (S::NT * 128) + r;
+      const int64_t i = rid / a.G, g = rid - i * a.G;
+      const int64_t orow = (w.t0 + i) * a.q_heads + w.h * a.G + g;
+      const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+#pragma unroll
+      for (int k = 0; k < V; k += 2)
+        if (lane * V + k < D)
+          *reinterpret_cast<uint32_t*>(a.out + orow * D + lane * V + k) = pack_bf16(o[k] * inv, o[k + 1] * inv);
+      if (lane == 0 && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host.
+// ---------------------------------------------------------------------------
+size_t al(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Plan {
+  int dp, nt, rows;            // padded head_dim, row tiles per item, rows kept per piece
+  size_t o, ml, open, total;   // scratch offsets and size
+};
+
+// NT = 2 shares every key and value tile between two row tiles and needs 256
+// rows to fill them; head_dim above 128 leaves TMEM and shared memory for one.
+// The lengths are device data, so the rule goes by the batch's average.
+Plan make_plan(const dg_kv_cache& c, const dg_kv_batch& b, int q_heads) {
+  Plan p;
+  p.dp = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
+  const int64_t rows = (int64_t)b.tokens * (q_heads / c.kv_heads);
+  p.nt = p.dp <= 128 && rows > 128ll * b.batch ? 2 : 1;
+  p.rows = (int)std::min<int64_t>(128 * p.nt, (rows + 7) / 8 * 8);
+  const size_t pieces = 2 * (size_t)kMaxCtas * p.rows;
+  p.o = 0;
+  p.ml = al(pieces * p.dp * 4);
+  p.open = p.ml + al(pieces * 8);
+  p.total = p.open + al(sizeof(Open) * kMaxCtas);
+  return p;
+}
+
+template <class S, bool F8>
+cudaError_t launch(const Args& a, int ctas, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(k_attend<S, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
+  if (e != cudaSuccess) return e;
+  k_attend<S, F8><<<ctas, S::THREADS, S::SMEM, s>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess || ctas == 1) return e;
+  // the join's launch overlaps the kernel's end; it waits for it on the device
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas - 1, (unsigned)std::min(16, (a.rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_join<S>, a);
 }
 
 }  // namespace attn
@@ -107,18 +974,23 @@ using namespace dg;
 
 extern "C" size_t dg_cache_attention_scratch_bytes(const dg_kv_cache* cache, const dg_kv_batch* batch,
                                                    int32_t q_heads) {
-  if (kv_check(cache, batch) || q_heads < 1 || q_heads % cache->kv_heads) return 0;
-  return 256;
+  if (kv_check(cache, batch)) return 0;
+  if (q_heads < 1 || q_heads % cache->kv_heads) {
+    fail(DG_EINVAL, "q_heads must be a multiple of kv_heads");
+    return 0;
+  }
+  return attn::make_plan(*cache, *batch, q_heads).total;
 }
 
 extern "C" int dg_cache_attention(const dg_kv_cache* cache, const dg_kv_batch* batch, int32_t q_heads,
                                   const void* q, int64_t q_ts, int64_t q_hs, float scale, int32_t mask,
                                   const uint32_t* tree_mask, int32_t mask_words, void* out, float* lse,
                                   void* scratch, size_t scratch_bytes, void* stream) {
+  using namespace attn;
   int rc = kv_check(cache, batch);
   if (rc) return rc;
   if (q_heads < 1 || q_heads % cache->kv_heads) return fail(DG_EINVAL, "q_heads must be a multiple of kv_heads");
-  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(DG_EINVAL, "scale must be positive and finite");
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f)) return fail(DG_EINVAL, "scale must be positive and finite");
   if (mask < DG_MASK_FULL || mask > DG_MASK_TREE) return fail(DG_EINVAL, "mask must be one of DG_MASK_*");
   if (mask == DG_MASK_TREE && (mask_words < 0 || (mask_words && !tree_mask)))
     return fail(DG_EINVAL, "DG_MASK_TREE needs tree_mask and mask_words >= 0");
@@ -126,14 +998,26 @@ extern "C" int dg_cache_attention(const dg_kv_cache* cache, const dg_kv_batch* b
   if ((rc = kv_row_args(q, q_ts, q_hs))) return rc;
   if (!out || off16(out)) return fail(DG_EINVAL, "out must be 16-byte aligned and not NULL");
   if (!scratch || reinterpret_cast<uintptr_t>(scratch) % 256) return fail(DG_EINVAL, "scratch must be 256-byte aligned and not NULL");
-  if (scratch_bytes < dg_cache_attention_scratch_bytes(cache, batch, q_heads))
-    return fail(DG_ENOMEM, "scratch is smaller than dg_cache_attention_scratch_bytes()");
-  const attn::Args a{{*cache, *batch}, static_cast<const __nv_bfloat16*>(q), q_ts, q_hs, q_heads,
-                     scale * 1.4426950408889634f, mask, tree_mask, mask_words,
-                     static_cast<__nv_bfloat16*>(out), lse};
-  const int64_t grid = ((int64_t)batch->tokens * q_heads + 7) / 8;
-  if (grid > 0x7fffffff) return fail(DG_EUNSUPPORTED, "too many rows");
-  if (cache->format == DG_KV_E4M3) attn::k_attend_rows<true><<<(unsigned)grid, 256, 0, (cudaStream_t)stream>>>(a);
-  else attn::k_attend_rows<false><<<(unsigned)grid, 256, 0, (cudaStream_t)stream>>>(a);
-  return kv_launched(cudaGetLastError());
+  const Plan p = make_plan(*cache, *batch, q_heads);
+  if (scratch_bytes < p.total) return fail(DG_ENOMEM, "scratch is smaller than dg_cache_attention_scratch_bytes()");
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return kv_launched(e);
+  char* sc = static_cast<char*>(scratch);
+  const Args a{{*cache, *batch}, static_cast<const __nv_bfloat16*>(q), q_ts, q_hs, q_heads,
+               q_heads / cache->kv_heads, scale * 1.4426950408889634f, mask, tree_mask, mask_words,
+               static_cast<__nv_bfloat16*>(out), lse, reinterpret_cast<float*>(sc + p.o),
+               reinterpret_cast<float2*>(sc + p.ml), reinterpret_cast<Open*>(sc + p.open), p.rows};
+  const int ctas = std::min(sms, kMaxCtas);
+  const bool f8 = cache->format == DG_KV_E4M3;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto go = [&](auto shape) {
+    using S = decltype(shape);
+    return f8 ? launch<S, true>(a, ctas, s) : launch<S, false>(a, ctas, s);
+  };
+  if (p.dp == 256) e = go(Shape<256, 1>());
+  else if (p.dp == 128) e = p.nt == 2 ? go(Shape<128, 2>()) : go(Shape<128, 1>());
+  else e = p.nt == 2 ? go(Shape<64, 2>()) : go(Shape<64, 1>());
+  return kv_launched(e);
 }

@@ -25,11 +25,13 @@ __device__ __forceinline__ void raise_status(int* status, int code) { atomicCAS(
 // entries are `table`; -1 if the position has no page (the status is raised).
 // The host has checked that the cache has fewer than 2^31 rows.
 __device__ __forceinline__ int kv_row(const KvView& w, const int32_t* table, int64_t pos, int head) {
-  const int64_t at = pos / w.c.page_size;
-  if (pos >= 0 && at < w.b.table_stride) {
-    const int page = __ldg(table + at);
-    if (page >= 0 && page < w.c.pages)
-      return (page * w.c.kv_heads + head) * w.c.page_size + (int)(pos - at * w.c.page_size);
+  if (pos >= 0 && pos <= 0x7fffffff) {         // the table covers fewer than 2^31 positions
+    const uint32_t at = (uint32_t)pos / (uint32_t)w.c.page_size;
+    if (at < (uint32_t)w.b.table_stride) {
+      const int page = __ldg(table + at);
+      if (page >= 0 && page < w.c.pages)
+        return (page * w.c.kv_heads + head) * w.c.page_size + (int)((uint32_t)pos - at * (uint32_t)w.c.page_size);
+    }
   }
   raise_status(w.c.status, DG_EINVAL);
   return -1;
