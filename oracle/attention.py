@@ -53,8 +53,8 @@ def dequantise(codes, exp):
 
 def attend(Q, K, V, seen, scale):
     """Query rows Q [R, D] over the positions each sees (bool [R, L]): (out [R, D], lse [R],
-    sum p |v| [R, D], largest sum |q k| scale of each row [R]). What a row does not see is left out
-    of its sums, not multiplied by zero."""
+    sum p |v| [R, D], largest sum |q k| scale of each row [R], root of the sum of (p v)^2 over
+    keys and columns [R]). What a row does not see is left out of its sums, not multiplied by zero."""
     with np.errstate(invalid="ignore", over="ignore", divide="ignore"):
         z = np.where(seen, Q @ K.T * scale, -np.inf)
         m = z.max(1, initial=-np.inf)
@@ -67,7 +67,8 @@ def attend(Q, K, V, seen, scale):
             out += np.where(seen[:, j, None], p[:, j, None] * np.where(fine[j], 0.0, V[j]), 0.0)
         size = p @ np.abs(np.where(fine, V, 0.0))
         logit = np.where(seen, np.abs(Q) @ np.abs(np.where(np.isfinite(K), K, 0.0)).T * scale, 0.0)
-        return out, m + np.log(l), size, logit.max(1, initial=0.0)
+        spread = np.sqrt((p * p) @ (np.where(fine, V, 0.0) ** 2).sum(1))
+        return out, m + np.log(l), size, logit.max(1, initial=0.0), spread
 
 
 def seen_by(i, past, new, mask, words=None):

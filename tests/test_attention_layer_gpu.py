@@ -264,7 +264,7 @@ def _check_attention(s, q, mask, scale, out, lse, words=None, rows=None):
         seen = np.stack([A.seen_by(i, p, n, mask, None if words is None else words[s.first[b] + i]) for i in at])
         L = seen.sum(1)
         for h in range(q.shape[1]):
-            want, wl, size, logit = A.attend(q[t, h], K[:, h // group], V[:, h // group], seen, float(scale))
+            want, wl, size, logit, spread = A.attend(q[t, h], K[:, h // group], V[:, h // group], seen, float(scale))
             got, gl = out[t, h], lse[t, h]
             assert not got[L == 0].any() and np.isneginf(gl[L == 0]).all(), (b, h)
             delta = (s.D * 2.0 ** -23 + 4 * U32) * logit
@@ -273,6 +273,13 @@ def _check_attention(s, q, mask, scale, out, lse, words=None, rows=None):
             assert np.array_equal(got[~fine], want[~fine], equal_nan=True), (b, h)
             err = np.abs(got - want)[fine] / tol[fine]
             assert (err <= 1).all(), (b, h, err.max())
+            # each probability's rounding is its own, uniform to u16 of p at most: over keys and columns
+            # the errors add as squares, at most u16 / sqrt(3) spread; three times that is far out
+            fine = np.isfinite(want).all(1)
+            norm = np.linalg.norm(got[fine] - want[fine], axis=1)
+            lim = (3 * (U16 / 3 ** 0.5 + 3 * delta) * spread + 2.0 ** -20 * size.sum(1)
+                   + U16 * np.linalg.norm(want, axis=1) + 1e-37)[fine]
+            assert (norm <= lim).all(), (b, h, (norm / lim).max())
             fine = np.isfinite(wl)
             err = np.abs(gl - wl)[fine] / (delta + 2.0 ** -21 + L * U32 + 4 * U32 * np.abs(wl))[fine]
             assert (err <= 1).all(), (b, h, err.max())
@@ -343,6 +350,18 @@ def test_attention_large_logits_and_growing_maxima():
     for scale in (0.01, 1.0, 4.0):
         out, lse = s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL, scale=scale)
         _check_attention(s, q, "causal", scale, out, lse)
+
+
+@pytest.mark.parametrize("fmt", [dg.DG_KV_BF16, dg.DG_KV_E4M3])
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 4), (256, 2)])
+def test_attention_single_tokens_of_a_ragged_batch(fmt, D, G):
+    """Few rows in each tile, several items to a CTA and several CTAs to an item."""
+    lengths = [(8000 - 233 * b, 1 if b % 8 != 7 else 0) for b in range(33)]
+    s = Setup(lengths, fmt, 4, D, 64, seed=D)
+    q = _tokens_q(s, G, 2)
+    out, lse = s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL)
+    s.cache.check()
+    _check_attention(s, q, "causal", D ** -0.5, out, lse)
 
 
 @pytest.mark.parametrize("fmt", [dg.DG_KV_BF16, dg.DG_KV_E4M3])

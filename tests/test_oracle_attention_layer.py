@@ -47,12 +47,12 @@ def test_attention_row_against_two_passes():
     assert seen.tolist() == [True] * 5 + [False, True, False, True]
     K[5] = np.nan
     V[7] = np.inf
-    out, lse, _, _ = A.attend(q[None], K, V, seen[None], 0.3)
+    out, lse, *_ = A.attend(q[None], K, V, seen[None], 0.3)
     e = np.exp(np.longdouble(0.3) * (K[seen].astype(np.longdouble) @ q))
     assert np.allclose(out[0], (e @ V[seen] / e.sum()).astype(float), atol=1e-14)
     assert abs(lse[0] - float(np.log(e.sum()))) < 1e-14
-    out, _, _, _ = A.attend(q[None], K, V, seen[None] | (np.arange(9) == 7), 0.3)
+    out, *_ = A.attend(q[None], K, V, seen[None] | (np.arange(9) == 7), 0.3)
     assert np.isposinf(out).all()
-    out, lse, _, _ = A.attend(q[None], K, V, np.zeros((1, 9), bool), 0.3)
+    out, lse, *_ = A.attend(q[None], K, V, np.zeros((1, 9), bool), 0.3)
     assert not out.any() and lse[0] == -np.inf
     assert A.seen_by(2, 1, 4, "causal").tolist() == [True, True, True, True, False]

@@ -543,6 +543,13 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     const uint32_t t_o = tmem + S::T_O + x * S::DP + lanes;
     bool ok = true;
     uint32_t gt = 0;                                  // key tiles done by this CTA
+    // P V of key tile k is complete. A parity wait must not start two phases
+    // ahead of its barrier: S of tile k is issued after P V of tile k - 1 with
+    // NT = 2, but only after that of k - 2 with NT = 1, which therefore
+    // alternates between two barriers.
+    auto pv_done = [&](uint32_t k) {
+      return S::NT == 2 ? wait(&sy.o_done[x], k & 1, sy, a) : wait(&sy.o_done[k & 1], (k >> 1) & 1, sy, a);
+    };
     int open_b = -1, open_h = 0, open_m = 0;          // an item begun and not finished
     int64_t open_end = 0;
     for (; w.more() && ok; w.next()) {
@@ -589,7 +596,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           const bool first = t == w.tb;
           const bool move = top > m + kGrow || (m == -INFINITY && top > m);
           if (!first && __any_sync(0xffffffffu, move && valid)) {
-            if (!__all_sync(0xffffffffu, wait(&sy.o_done[x], (gt - 1) & 1, sy, a))) { ok = false; break; }
+            if (!__all_sync(0xffffffffu, pv_done(gt - 1))) { ok = false; break; }
             tc_fence_after();
             const float f = move ? ex2(m - top) : 1.f;
             l *= f;
@@ -636,7 +643,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       }
       if (!ok) break;
       // ---------------------------------------------------------- the segment's result
-      if (!__all_sync(0xffffffffu, wait(&sy.o_done[x], (gt - 1) & 1, sy, a))) { ok = false; break; }
+      if (!__all_sync(0xffffffffu, pv_done(gt - 1))) { ok = false; break; }
       const bool whole = w.tb == 0 && w.te == w.T;
       const bool fix = a.mask != DG_MASK_FULL && *(volatile int*)&sy.nonfinite;
       const int piece = blockIdx.x * 2 + (w.tb == 0 ? 1 : 0);
@@ -647,6 +654,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
 #pragma unroll 1
         for (int c = 0; c < S::DP / 32; ++c) {
           float o[32];
+          __syncwarp();                               // the lanes part below; TMEM loads take all of them
           tmem_ld32(t_o + c * 32, o);
           if (fix && valid) {
             // what load_rows left out, for the rows that do see it
@@ -665,8 +673,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
               }
             }
           }
-          if (!valid) continue;
-          if (whole) {
+          if (valid && whole) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               if (c * 32 + k * 8 >= a.w.c.head_dim) break;
@@ -677,7 +684,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
               v.w = pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv);
               *reinterpret_cast<uint4*>(a.out + orow * a.w.c.head_dim + c * 32 + k * 8) = v;
             }
-          } else {
+          } else if (valid) {
             float* dst = a.part_o + ((int64_t)piece * a.rows + r) * S::DP + c * 32;
 #pragma unroll
             for (int k = 0; k < 32; k += 4)
@@ -686,6 +693,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
         }
         if (valid && whole && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         if (valid && !whole) a.part_ml[(int64_t)piece * a.rows + r] = make_float2(m, l);
+        __syncwarp();
         tc_fence_before();
       }
       if (w.tb == 0 && w.te < w.T) {
@@ -770,7 +778,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
         for (int k = 0; k < BN / 16; ++k)
           mma_bf16_ts(tmem + S::T_O + x * S::DP, tmem + buf * S::T_S + k * 8,
                       sdesc(v0 + k * 2048, BN * 128, 1024), id_o, first && k == 0 ? 0u : 1u);
-        mma_commit(&sy.o_done[x]);
+        mma_commit(&sy.o_done[S::NT == 2 ? x : buf]);
       };
       for (; w.more() && ok; w.next(), ++seg) {
         if (!wait(&sy.q_full, seg & 1, sy, a) || !slot_full(e)) { ok = false; break; }
