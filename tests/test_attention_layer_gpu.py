@@ -410,6 +410,21 @@ def test_what_is_masked_does_not_touch_a_row(fmt, D, G, new):
         assert out[1:, :, rest].float().isfinite().all()
 
 
+@pytest.mark.parametrize("G,new", [(1, 1), (8, 1), (8, 30)])
+def test_infinite_values_of_the_past_come_out(G, new):
+    s = Setup([(500, new), (40, new)], dg.DG_KV_BF16, 1, 128, 16, seed=G)
+    q = _tokens_q(s, G, 5)
+    want, lse = s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL)
+    for pos, d, x in ((3, 7, float("inf")), (300, 9, -float("inf")), (499, 11, float("nan")), (77, 7, 1.0)):
+        page, place = s.at(0, pos, pos + 1)
+        s.cache.v[page, :, place, d] = x
+    out, lse2 = s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL)
+    assert (out[:new, :, 7] == float("inf")).all() and (out[:new, :, 9] == -float("inf")).all()
+    assert out[:new, :, 11].isnan().all() and torch.equal(lse, lse2)
+    rest = [d for d in range(128) if d not in (7, 9, 11)]
+    assert torch.equal(out[:, :, rest], want[:, :, rest]) and torch.equal(out[new:], want[new:])
+
+
 def test_attention_reports_bad_pages():
     s = Setup([(40, 2)], dg.DG_KV_BF16, 1, 64, 16, seed=2)
     q = _tokens_q(s, 2)

@@ -66,7 +66,9 @@ struct Args {
   KvView w;
   const __nv_bfloat16* q;
   int64_t q_ts, q_hs;
-  int q_heads, G;
+  int q_heads, G;              // G query heads per key/value head
+  uint32_t g_mul;              // r / G = r g_mul >> g_shift, exact for r < 2^31
+  int g_shift;
   float scale_log2;            // scale log2(e)
   int mask;
   const uint32_t* tree;
@@ -78,28 +80,38 @@ struct Args {
   float2* part_ml;             // [CTAs][2][rows] their m (log2 units) and l
   struct Open* open;           // [CTAs] the item a CTA begins and does not finish
   int rows;                    // rows kept per piece
+
+  __device__ __forceinline__ uint32_t over_g(uint32_t r) const {
+    return (uint32_t)(((uint64_t)r * g_mul) >> g_shift);
+  }
 };
 
-// The item that a CTA's share ends inside, if it also begins there.
+// The item that a CTA's share ends inside, if it also begins there: rows (0:
+// none), the CTAs it lies in, the sequence's first token, head and item index.
 struct Open {
-  int on, b, h, m;
-  int64_t end;                 // of the item, in the list of key tiles
-  int64_t share;               // key tiles per CTA
+  int rows, pieces, t0, h, m;
 };
 
-template <int DP_, int NT_>
+template <int DP_, int NT_, bool F8_>
 struct Shape {
+  static constexpr bool F8 = F8_;                      // e4m3 cache
   static constexpr int DP = DP_;                       // head_dim padded to 64, 128 or 256
   static constexpr int NT = NT_;
   static constexpr int BN = DP == 256 ? 64 : 128;      // keys per tile
-  static constexpr int SL = DP == 64 ? 6 : 4;          // ring slots (and load warps)
+  static constexpr int SL = DP == 256 ? 4 : DP == 128 ? (NT == 2 ? 4 : 5) : (NT == 2 ? 6 : 8);   // ring slots
+  // load warps per slot: converting e4m3 codes takes one warp longer than a
+  // slot's share of the memory bandwidth
+  static constexpr int LW = F8 && NT == 1 && DP > 64 ? 2 : 1;
+  // A tile of at most 32 rows, NT = 1 and 128 keys: see k_attend.
+  static constexpr bool FEW = NT == 1 && BN == 128;
   static constexpr int SLOT = BN * DP * 2;
   static constexpr int QTILE = 128 * DP * 2;
-  static constexpr int W_LOAD = NT * 4, W_Q = W_LOAD + SL, W_MMA = W_Q + 1;
+  static constexpr int W_LOAD = NT * 4, W_Q = W_LOAD + SL * LW, W_MMA = W_Q + 1;
   static constexpr int THREADS = (W_MMA + 1) * 32;
   static constexpr int T_S = NT == 2 ? 128 : BN;       // TMEM columns between S buffers
   static constexpr int T_O = NT == 2 ? 256 : 2 * BN;   // first column of O
-  static constexpr size_t SMEM = 1024 + (size_t)NT * QTILE + (size_t)SL * SLOT + 512 + 8 * (kMaxBatch + 1);
+  static constexpr size_t SMEM = 1024 + (size_t)NT * QTILE + (size_t)SL * SLOT + (FEW ? 4 * 32 * 64 + 4 * 32 * 8 : 0) + 512;
+  static_assert(8 * (kMaxBatch + 1) <= SL * SLOT, "the plan's sums lie in the ring before it is used");
   static_assert(T_O + NT * DP <= TMEM_COLS, "TMEM");
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -121,21 +133,19 @@ struct Walk {
     n = kv_new(a.w, b, &t0);
     past = kv_past(a.w, b, n);
   }
-  __device__ __forceinline__ int items() const { return (int)(((int64_t)n * a.G + ROWS - 1) / ROWS); }
+  // (Rows and positions are below 2^31, so that 32-bit arithmetic serves: a
+  // 64-bit division here and in the query loads had cost more than the tiles.)
+  __device__ __forceinline__ int items() const { return (int)(((uint32_t)n * (uint32_t)a.G + ROWS - 1) / ROWS); }
   // Key tiles of item x: up to its last row's token under a causal mask, else all; at least one.
   __device__ __forceinline__ int tiles(int x) const {
-    int64_t e = n;
-    if (a.mask == DG_MASK_CAUSAL) {
-      const int64_t upto = ((int64_t)(x + 1) * ROWS + a.G - 1) / a.G;
-      e = upto < e ? upto : e;
-    }
-    const int64_t t = ((int64_t)past + e + BN - 1) / BN;
-    return t < 1 ? 1 : (int)t;
+    uint32_t e = (uint32_t)n;
+    if (a.mask == DG_MASK_CAUSAL) e = min(e, a.over_g((uint32_t)(x + 1) * ROWS + (uint32_t)a.G - 1));
+    return (int)max(1u, ((uint32_t)past + e + BN - 1) / BN);
   }
   __device__ __forceinline__ int64_t keys() const { return (int64_t)past + n; }
   // First position that some row of the item may not see.
   __device__ __forceinline__ int64_t clear() const {
-    return a.mask == DG_MASK_FULL ? keys() : a.mask == DG_MASK_TREE ? past : past + (int64_t)m * ROWS / a.G + 1;
+    return a.mask == DG_MASK_FULL ? keys() : a.mask == DG_MASK_TREE ? past : (int64_t)past + a.over_g((uint32_t)m * ROWS) + 1;
   }
   __device__ __forceinline__ bool more() const { return pos < hi; }
   __device__ __forceinline__ void next() {
@@ -153,8 +163,7 @@ struct Walk {
     te = (int)(T < hi - pos ? T : hi - pos);
   }
   __device__ __forceinline__ int rows() const {
-    const int64_t r = (int64_t)n * a.G - (int64_t)m * ROWS;
-    return r < ROWS ? (int)r : ROWS;
+    return min(n * a.G - m * ROWS, ROWS);
   }
 };
 
@@ -263,6 +272,7 @@ struct Sync {
   uint64_t s_full[2], p_full[2];   // S ready; P stored
   uint64_t o_done[2], o_free[2];   // P V done; O read
   uint64_t q_full, q_free, fin;
+  uint64_t merge;                  // between the four warps that share a tile's rows
   uint32_t tmem;
   int abort, nonfinite;
   Start start;
@@ -299,6 +309,16 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// 16 columns of TMEM to each lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 // 16 registers of each lane to 16 columns of TMEM.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
@@ -375,42 +395,53 @@ __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t pair, float scale) {
   return pack_bf16(f.x * scale, f.y * scale);
 }
 
-// One warp fills one ring slot with the BN key (or value) rows from position
-// j0 on. `clean`: rows that a query row of the item may not see hold values
-// that must not reach it; what is not finite is then replaced by zero and
-// noted (0 x NaN in the second product would reach every row).
-template <class S, bool F8, typename W>
-__device__ __forceinline__ void load_rows(const W& w, const void* pages, const uint8_t* exps, int64_t j0,
-                                          uint32_t dst, bool clean, Sync& sy) {
-  constexpr int PER = S::BN / 32;
+// The cache rows of this warp's share of a key tile: rows lane, lane + 32, ...
+// of the BN / LW from position j0 on; -1 beyond the sequence or without a page.
+template <class S, typename W>
+__device__ __forceinline__ void find_rows(const W& w, int64_t j0, int* row) {
+  const int32_t* table = w.a.w.b.page_table + (int64_t)w.b * w.a.w.b.table_stride;
+  const int64_t L = w.keys();
+#pragma unroll
+  for (int p = 0; p < S::BN / S::LW / 32; ++p) {
+    const int64_t j = j0 + p * 32 + (threadIdx.x & 31);
+    row[p] = j < L ? kv_row(w.a.w, table, j, w.h) : -1;
+  }
+}
+
+// One warp fills its share of a ring slot (rows r0 to r0 + BN / LW) with key or
+// value rows. `clean`: the tile holds positions that a query row of the item
+// may not see; what is not finite there is replaced by zero and noted (0 x NaN
+// in the second product would reach every row).
+//
+// e4m3: the codes are copied into the upper half of the warp's part of the slot
+// and converted in place. In order of 64-column blocks and rows, 16 codes at
+// offset x of the codes become 32 bytes at offset 2x of the part, which holds
+// only codes already read; so the whole tile is in flight at once, without
+// registers or a staging buffer.
+template <class S, typename W>
+__device__ __forceinline__ void load_rows(const W& w, const void* pages, const uint8_t* exps, const int* row,
+                                          int r0, uint32_t slot, bool clean, Sync& sy) {
+  constexpr int RW = S::BN / S::LW;
   const Args& a = w.a;
   const int lane = threadIdx.x & 31;
   const int D = a.w.c.head_dim;
-  const int32_t* table = a.w.b.page_table + (int64_t)w.b * a.w.b.table_stride;
-  const int64_t L = w.keys();
-  int row[PER];                                    // rows lane, lane + 32, ...: cache row or -1
-#pragma unroll
-  for (int p = 0; p < PER; ++p) {
-    const int64_t j = j0 + p * 32 + lane;
-    row[p] = j < L ? kv_row(a.w, table, j, w.h) : -1;
-  }
-  if constexpr (!F8) {
+  if constexpr (!S::F8) {
     constexpr int CPR = S::DP / 8, RPI = 32 / CPR; // chunks per row, rows per instruction
     const int c = lane % CPR;
     const bool in = c * 8 < D;
     const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(pages) + c * 8;
 #pragma unroll
-    for (int it = 0; it < S::BN / RPI; ++it) {
+    for (int it = 0; it < RW / RPI; ++it) {
       const int r = it * RPI + lane / CPR;
       const int cr = __shfl_sync(0xffffffffu, row[it * RPI / 32], r & 31);
       const bool on = in && cr >= 0;
-      copy16(dst + swizzled(r, c, S::BN), on ? base + (int64_t)cr * D : a.q, on ? 16 : 0);
+      copy16(slot + swizzled(r0 + r, c, S::BN), on ? base + (int64_t)cr * D : a.q, on ? 16 : 0);
     }
     copies_landed();
     if (clean) {
       bool dirty = false;
-      for (int it = 0; it < S::BN / RPI; ++it) {
-        const uint32_t at = dst + swizzled(it * RPI + lane / CPR, c, S::BN);
+      for (int it = 0; it < RW / RPI; ++it) {
+        const uint32_t at = slot + swizzled(r0 + it * RPI + lane / CPR, c, S::BN);
         const uint4 v = ld_shared(at);
         const uint4 f = make_uint4(only_finite(v.x), only_finite(v.y), only_finite(v.z), only_finite(v.w));
         if (f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w) {
@@ -421,71 +452,110 @@ __device__ __forceinline__ void load_rows(const W& w, const void* pages, const u
       if (dirty) *(volatile int*)&sy.nonfinite = 1;
     }
   } else {
-    constexpr int CPR = S::DP / 16, RPI = 32 / CPR, N = S::BN / RPI, BATCH = 8;
-    const int c = lane % CPR;
-    const bool in = c * 16 < D;
-    const uint8_t* base = static_cast<const uint8_t*>(pages) + c * 16;
-    float scale[PER];
+    constexpr int NB = S::DP / 64, HALF = RW * 64, PER = RW / 8, N = NB * PER, BATCH = 4;
+    const int q = lane & 3, rl = lane >> 2;        // 16-code chunk of a block's row; row of 8
+    const uint8_t* base = static_cast<const uint8_t*>(pages) + q * 16;
+    // byte `lin` of the warp's part: blocks of 2 HALF bytes, BN rows apart in the slot
+    auto part = [&](uint32_t lin) { return slot + lin / (2 * HALF) * (S::BN * 128) + r0 * 128 + lin % (2 * HALF); };
+    float scale[RW / 32];
 #pragma unroll
-    for (int p = 0; p < PER; ++p)
+    for (int p = 0; p < RW / 32; ++p)
       scale[p] = row[p] >= 0 ? __uint_as_float(max(1u, min(254u, (uint32_t)__ldg(exps + row[p]))) << 23) : 0.f;
+#pragma unroll
+    for (int it = 0; it < N; ++it) {
+      const int cb = it / PER, r = it % PER * 8 + rl;
+      const int cr = __shfl_sync(0xffffffffu, row[it % PER * 8 / 32], r & 31);
+      const bool on = cr >= 0 && cb * 64 + q * 16 < D;
+      copy16(part(NB * HALF + cb * HALF + it % PER * 512) + lane * 16, on ? base + (int64_t)cr * D + cb * 64 : (const void*)a.q,
+             on ? 16 : 0);
+    }
+    copies_landed();
+    __syncwarp();
 #pragma unroll
     for (int i0 = 0; i0 < N; i0 += BATCH) {
       uint4 v[BATCH];
 #pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
-        const int r = (i0 + k) * RPI + lane / CPR;
-        const int cr = __shfl_sync(0xffffffffu, row[(i0 + k) * RPI / 32], r & 31);
-        v[k] = make_uint4(0, 0, 0, 0);
-        if (in && cr >= 0) v[k] = __ldg(reinterpret_cast<const uint4*>(base + (int64_t)cr * D));
-      }
+      for (int k = 0; k < BATCH; ++k)
+        v[k] = ld_shared(part(NB * HALF + (i0 + k) / PER * HALF + (i0 + k) % PER * 512) + lane * 16);
+      __syncwarp();
 #pragma unroll
       for (int k = 0; k < BATCH; ++k) {
-        const int r = (i0 + k) * RPI + lane / CPR;
-        const float s = __shfl_sync(0xffffffffu, scale[(i0 + k) * RPI / 32], r & 31);
+        const int cb = (i0 + k) / PER, r = (i0 + k) % PER * 8 + rl;
+        const float f = __shfl_sync(0xffffffffu, scale[(i0 + k) % PER * 8 / 32], r & 31);
         const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
         uint32_t o[8];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          o[2 * t] = codes_to_bf16(x[t], s);
-          o[2 * t + 1] = codes_to_bf16(x[t] >> 16, s);
+          o[2 * t] = codes_to_bf16(x[t], f);
+          o[2 * t + 1] = codes_to_bf16(x[t] >> 16, f);
         }
         if (clean) {
           bool dirty = false;
 #pragma unroll
           for (int t = 0; t < 8; ++t) {
-            const uint32_t f = only_finite(o[t]);
-            dirty |= f != o[t];
-            o[t] = f;
+            const uint32_t g = only_finite(o[t]);
+            dirty |= g != o[t];
+            o[t] = g;
           }
           if (dirty) *(volatile int*)&sy.nonfinite = 1;
         }
-        st_shared(dst + swizzled(r, 2 * c, S::BN), make_uint4(o[0], o[1], o[2], o[3]));
-        st_shared(dst + swizzled(r, 2 * c + 1, S::BN), make_uint4(o[4], o[5], o[6], o[7]));
+        st_shared(slot + swizzled(r0 + r, cb * 8 + 2 * q, S::BN), make_uint4(o[0], o[1], o[2], o[3]));
+        st_shared(slot + swizzled(r0 + r, cb * 8 + 2 * q + 1, S::BN), make_uint4(o[4], o[5], o[6], o[7]));
       }
+      __syncwarp();
     }
   }
 }
 
-// What load_rows left out of value columns d .. d + 7 of a cache row: its
-// infinities and NaN, zero elsewhere.
-template <bool F8>
-__device__ __forceinline__ void not_finite8(const Args& a, int row, int d, float* v) {
-  const int64_t at = (int64_t)row * a.w.c.head_dim + d;
-  if constexpr (F8) {
-    const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.w.c.v) + at);
+// o (columns d .. d + 3 of a row's sum) with the infinities and NaN among the
+// values that new token i of the sequence sees in the segment's keys from
+// position `from` on. They decide the result wherever there are any: load_rows
+// has left them out, or a product with P = 0 has made a NaN of them.
+template <class S, typename W>
+__device__ __noinline__ float4 with_not_finite(const W w, const uint32_t* tree, int i, int d, int64_t from, float4 o) {
+  const Args& a = w.a;
+  if (d >= a.w.c.head_dim) return o;
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
+  const int64_t end = min(w.keys(), (int64_t)w.te * S::BN);
+  for (int64_t j = max(from, (int64_t)w.tb * S::BN); j < end; ++j) {
+    if (!(seen(w, tree, i, j) & 1)) continue;
+    const int row = kv_row(a.w, a.w.b.page_table + (int64_t)w.b * a.w.b.table_stride, j, w.h);
+    if (row < 0) continue;
+    const int64_t at = (int64_t)row * a.w.c.head_dim + d;
+    if constexpr (S::F8) {
+      const uint32_t c = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.w.c.v) + at);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t code = (j < 4 ? c.x : c.y) >> (8 * (j & 3));
-      v[j] = (code & 0x7f) == 0x7f ? NAN : 0.f;
+      for (int k = 0; k < 4; ++k) if ((c >> (8 * k) & 0x7f) == 0x7f) x[k] = NAN;
+    } else {
+      const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.w.c.v) + at);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t half = (k < 2 ? c.x : c.y) >> (16 * (k & 1)) & 0xffffu;
+        if (!finite_bf16(half)) x[k] += __uint_as_float(half << 16);
+      }
     }
-  } else {
-    const uint4 c = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.w.c.v) + at);
-    const uint32_t x[4] = {c.x, c.y, c.z, c.w};
+  }
+  return make_float4(x[0] == 0.f ? o.x : x[0], x[1] == 0.f ? o.y : x[1], x[2] == 0.f ? o.z : x[2],
+                     x[3] == 0.f ? o.w : x[3]);
+}
+
+// A 4 x 4 transposition of 16-byte pieces over each four lanes: lane q of four
+// leaves with piece q of the four lanes' rows.
+__device__ __forceinline__ void transpose4(uint4* v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t half = x[j >> 1] >> (16 * (j & 1)) & 0xffffu;
-      v[j] = finite_bf16(half) ? 0.f : __uint_as_float(half << 16);
+  for (int d = 1; d < 4; d <<= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & d) continue;
+      uint4 t = up ? v[i] : v[i | d];
+      t.x = __shfl_xor_sync(0xffffffffu, t.x, d);
+      t.y = __shfl_xor_sync(0xffffffffu, t.y, d);
+      t.z = __shfl_xor_sync(0xffffffffu, t.z, d);
+      t.w = __shfl_xor_sync(0xffffffffu, t.w, d);
+      if (up) v[i] = t;
+      else v[i | d] = t;
     }
   }
 }
@@ -493,7 +563,14 @@ __device__ __forceinline__ void not_finite8(const Args& a, int row, int d, float
 // ---------------------------------------------------------------------------
 // The kernel.
 // ---------------------------------------------------------------------------
-template <class S, bool F8>
+//
+// Few rows. A tile of at most 32 rows (NT = 1, 128 keys) would leave three of
+// the four softmax warps idle and one with all 128 columns. Its rows are laid
+// into the tile four times instead, and warp k takes columns 32 k to 32 k + 31
+// of its copy: P is zero in the others, so that O of copy k is the sum over a
+// quarter of the keys, with an m and l of its own. The four are joined at the
+// end of the item.
+template <class S>
 __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant__ Args a) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem =
@@ -501,12 +578,14 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
   unsigned char* ring = smem + S::NT * S::QTILE;
   Sync& sy = *reinterpret_cast<Sync*>(ring + S::SL * S::SLOT);
   static_assert(sizeof(Sync) <= 512, "barriers");
-  int64_t* pref = reinterpret_cast<int64_t*>(ring + S::SL * S::SLOT + 512);
+  float* few_o = reinterpret_cast<float*>(ring + S::SL * S::SLOT + 512);         // [4][32][16]
+  float2* few_ml = reinterpret_cast<float2*>(few_o + 4 * 32 * 16);              // [4][32]
+  int64_t* pref = reinterpret_cast<int64_t*>(ring);
   constexpr int ROWS = S::NT * 128, BN = S::BN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S::SL; ++s) { mbar_init(&sy.full[s], 1); mbar_init(&sy.empty[s], 1); }
+    for (int s = 0; s < S::SL; ++s) { mbar_init(&sy.full[s], S::LW); mbar_init(&sy.empty[s], 1); }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sy.s_full[x], 1);
       mbar_init(&sy.p_full[x], 4);
@@ -516,6 +595,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     mbar_init(&sy.q_full, 1);
     mbar_init(&sy.q_free, 1);
     mbar_init(&sy.fin, 1);
+    mbar_init(&sy.merge, 4);
     sy.abort = 0;
     sy.nonfinite = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -538,7 +618,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     // ---------------------------------------------------------------- softmax
     const int x = warp >> 2;                          // row tile
     const int quarter = warp & 3;
-    const int r = x * 128 + quarter * 32 + lane;      // row within the item
+    const int r = x * 128 + quarter * 32 + lane;      // row of the tiles
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t t_o = tmem + S::T_O + x * S::DP + lanes;
     bool ok = true;
@@ -550,14 +630,16 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     auto pv_done = [&](uint32_t k) {
       return S::NT == 2 ? wait(&sy.o_done[x], k & 1, sy, a) : wait(&sy.o_done[k & 1], (k >> 1) & 1, sy, a);
     };
-    int open_b = -1, open_h = 0, open_m = 0;          // an item begun and not finished
-    int64_t open_end = 0;
+    Open open{0, 0, 0, 0, 0};                         // an item begun and not finished
+    uint32_t merges = 0;
     for (; w.more() && ok; w.next()) {
       const int rows = w.rows();
-      const bool any = x * 128 + quarter * 32 < rows; // warp-uniform
-      const bool valid = r < rows;
-      const int64_t rid = (int64_t)w.m * ROWS + (valid ? r : 0);
-      const int i = (int)(rid / a.G), g = (int)(rid - (int64_t)i * a.G);
+      const bool few = S::FEW && rows <= 32;
+      const bool any = few || x * 128 + quarter * 32 < rows;     // warp-uniform
+      const int rr = few ? lane : r;                  // row within the item
+      const bool valid = rr < rows;
+      const uint32_t rid = (uint32_t)w.m * ROWS + (valid ? rr : 0);
+      const int i = (int)a.over_g(rid), g = (int)(rid - (uint32_t)i * a.G);
       const uint32_t* tree = a.mask == DG_MASK_TREE ? a.tree + (int64_t)(w.t0 + i) * a.words : nullptr;
       // tiles that reach beyond this position hold some that the row may not see
       const int64_t clear = a.mask == DG_MASK_FULL ? w.keys() : a.mask == DG_MASK_CAUSAL ? (int64_t)w.past + i + 1 : w.past;
@@ -571,17 +653,17 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           const uint32_t t_s = tmem + buf * S::T_S + lanes;
           const int64_t j0 = (int64_t)t * BN;
           const bool masked = __any_sync(0xffffffffu, j0 + BN > clear);
-          uint32_t word[BN / 32];
-#pragma unroll
-          for (int c = 0; c < BN / 32; ++c) word[c] = masked ? seen(w, tree, i, j0 + c * 32) : 0xffffffffu;
+          // chunks of 32 columns: all of them, or this warp's own
+          const int c0 = few ? quarter : 0, c1 = few ? quarter + 1 : BN / 32;
+          float s[32];
           float top = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < BN / 32; ++c) {
-            float s[32];
+#pragma unroll 1
+          for (int c = c0; c < c1; ++c) {
             tmem_ld32(t_s + c * 32, s);
             if (masked) {
+              const uint32_t word = seen(w, tree, i, j0 + c * 32);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) s[j] = (word[c] >> j) & 1 ? s[j] : -INFINITY;
+              for (int j = 0; j < 32; ++j) s[j] = (word >> j) & 1 ? s[j] : -INFINITY;
             }
             float u0 = -INFINITY, u1 = -INFINITY;
 #pragma unroll
@@ -615,13 +697,15 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           if (move) m = top;
           const float sub = m == -INFINITY ? 0.f : m;  // a row that has seen nothing yet: P = 0
           float l0 = 0.f, l1 = 0.f;
+#pragma unroll 1
+          for (int c = c0; c < c1; ++c) {
+            if (!few) {                               // one chunk is still in registers
+              tmem_ld32(t_s + c * 32, s);
+              if (masked) {
+                const uint32_t word = seen(w, tree, i, j0 + c * 32);
 #pragma unroll
-          for (int c = 0; c < BN / 32; ++c) {
-            float s[32];
-            tmem_ld32(t_s + c * 32, s);
-            if (masked) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) s[j] = (word[c] >> j) & 1 ? s[j] : -INFINITY;
+                for (int j = 0; j < 32; ++j) s[j] = (word >> j) & 1 ? s[j] : -INFINITY;
+              }
             }
             uint32_t p[16];
 #pragma unroll
@@ -633,6 +717,11 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
               p[j >> 1] = pack_bf16(e0, e1);
             }
             tmem_st16(t_s + c * 16, p);
+          }
+          if (S::FEW && few) {
+            const uint32_t zero[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+            for (int c = 1; c < 4; ++c) tmem_st16(t_s + ((quarter + c) & 3) * 16, zero);
           }
           l += l0 + l1;
           tmem_st_wait();
@@ -647,85 +736,162 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       const bool whole = w.tb == 0 && w.te == w.T;
       const bool fix = a.mask != DG_MASK_FULL && *(volatile int*)&sy.nonfinite;
       const int piece = blockIdx.x * 2 + (w.tb == 0 ? 1 : 0);
-      if (any) {
-        tc_fence_after();
+      const int orow = (w.t0 + i) * a.q_heads + w.h * a.G + g;
+      const int64_t prow = (int64_t)piece * a.rows + rr;
+      tc_fence_after();
+      if (S::FEW && few) {
+        // join the four copies: m and l through shared memory, O in chunks of 16 columns;
+        // thread (row, 4 columns) adds the copies
+        auto meet = [&]() {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sy.merge);
+          return __all_sync(0xffffffffu, wait(&sy.merge, merges++ & 1, sy, a)) != 0;
+        };
+        few_ml[quarter * 32 + lane] = make_float2(m, l);
+        if (!meet()) { ok = false; break; }
+        const int t = quarter * 32 + lane, fr = t >> 2, fc = (t & 3) * 4;
+        float f[4], fm = -INFINITY, fl = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) fm = fmaxf(fm, few_ml[k * 32 + fr].x);
+        const float sub = fm == -INFINITY ? 0.f : fm;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 ml = few_ml[k * 32 + fr];
+          f[k] = ex2(ml.x - sub);
+          fl += f[k] * ml.y;
+        }
+        const bool on = fr < rows;
+        const uint32_t frid = (uint32_t)w.m * ROWS + (on ? fr : 0);
+        const int fi = (int)a.over_g(frid);
+        const int frow = (w.t0 + fi) * a.q_heads + w.h * a.G + (int)(frid - (uint32_t)fi * a.G);
+        const uint32_t* ftree = a.mask == DG_MASK_TREE ? a.tree + (int64_t)(w.t0 + fi) * a.words : nullptr;
+        const float inv = fl > 0.f ? 1.f / fl : fl == 0.f ? 0.f : fl;
+#pragma unroll 1
+        for (int c = 0; c < S::DP / 16; ++c) {
+          uint32_t o[16];
+          tmem_ld16(t_o + c * 16, o);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(few_o + (quarter * 32 + lane) * 16 + ((k + lane) & 3) * 4) =
+                make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          if (!meet()) { ok = false; break; }
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 u = *reinterpret_cast<const float4*>(few_o + (k * 32 + fr) * 16 + (((t & 3) + fr) & 3) * 4);
+            v[0] = fmaf(u.x, f[k], v[0]);
+            v[1] = fmaf(u.y, f[k], v[1]);
+            v[2] = fmaf(u.z, f[k], v[2]);
+            v[3] = fmaf(u.w, f[k], v[3]);
+          }
+          if (on) {
+            // (the copies that do not take a key multiply its value by zero)
+            const bool off = !(fabsf(v[0]) + fabsf(v[1]) + fabsf(v[2]) + fabsf(v[3]) < INFINITY);
+            if (fix || off) {
+              const float4 u = with_not_finite<S>(w, ftree, fi, c * 16 + fc, off ? 0 : w.clear() / BN * BN,
+                                                  make_float4(v[0], v[1], v[2], v[3]));
+              v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+            }
+            if (!whole)
+              *reinterpret_cast<float4*>(a.part_o + ((int64_t)piece * a.rows + fr) * S::DP + c * 16 + fc) =
+                  make_float4(v[0], v[1], v[2], v[3]);
+            else if (c * 16 < a.w.c.head_dim)
+              *reinterpret_cast<uint2*>(a.out + (int64_t)frow * a.w.c.head_dim + c * 16 + fc) =
+                  make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
+          }
+          if (!meet()) { ok = false; break; }
+        }
+        if (!ok) break;
+        if (on && fc == 0) {
+          if (!whole) a.part_ml[(int64_t)piece * a.rows + fr] = make_float2(fm, fl);
+          else if (a.lse) a.lse[frow] = fl == 0.f ? -INFINITY : (fm + log2f(fl)) * kLn2;
+        }
+      } else if (any) {
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-        const int64_t orow = (int64_t)(w.t0 + i) * a.q_heads + w.h * a.G + g;
+        // stores by fours of lanes, 64 contiguous bytes of a row each
+        const int four = lane & ~3, q = lane & 3;
 #pragma unroll 1
         for (int c = 0; c < S::DP / 32; ++c) {
           float o[32];
           __syncwarp();                               // the lanes part below; TMEM loads take all of them
           tmem_ld32(t_o + c * 32, o);
           if (fix && valid) {
-            // what load_rows left out, for the rows that do see it
-            const int64_t k1 = min(w.keys(), (int64_t)w.te * BN);
-            for (int64_t j = max(w.clear() / BN * BN, (int64_t)w.tb * BN); j < k1; ++j) {
-              if (!(seen(w, tree, i, j) & 1)) continue;
-              const int row = kv_row(a.w, a.w.b.page_table + (int64_t)w.b * a.w.b.table_stride, j, w.h);
-              if (row < 0) continue;
 #pragma unroll
-              for (int d = 0; d < 32; d += 8) {
-                if (c * 32 + d >= a.w.c.head_dim) break;
-                float v[8];
-                not_finite8<F8>(a, row, c * 32 + d, v);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) o[d + k] += v[k];
-              }
+            for (int d = 0; d < 32; d += 4) {
+              const float4 u = with_not_finite<S>(w, tree, i, c * 32 + d, w.clear() / BN * BN,
+                                                  make_float4(o[d], o[d + 1], o[d + 2], o[d + 3]));
+              o[d] = u.x; o[d + 1] = u.y; o[d + 2] = u.z; o[d + 3] = u.w;
             }
           }
-          if (valid && whole) {
+          __syncwarp();
+          if (whole) {
+            uint4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              v[k] = make_uint4(pack_bf16(o[8 * k] * inv, o[8 * k + 1] * inv),
+                                pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                                pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                                pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+            transpose4(v);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              if (c * 32 + k * 8 >= a.w.c.head_dim) break;
-              uint4 v;
-              v.x = pack_bf16(o[8 * k] * inv, o[8 * k + 1] * inv);
-              v.y = pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv);
-              v.z = pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv);
-              v.w = pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv);
-              *reinterpret_cast<uint4*>(a.out + orow * a.w.c.head_dim + c * 32 + k * 8) = v;
+              const int to = __shfl_sync(0xffffffffu, valid ? orow : -1, four + k);
+              if (to >= 0 && c * 32 + q * 8 < a.w.c.head_dim)
+                *reinterpret_cast<uint4*>(a.out + (int64_t)to * a.w.c.head_dim + c * 32 + q * 8) = v[k];
             }
-          } else if (valid) {
-            float* dst = a.part_o + ((int64_t)piece * a.rows + r) * S::DP + c * 32;
+          } else {
 #pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<float4*>(dst + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            for (int h = 0; h < 2; ++h) {
+              uint4 v[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                v[k] = make_uint4(__float_as_uint(o[16 * h + 4 * k]), __float_as_uint(o[16 * h + 4 * k + 1]),
+                                  __float_as_uint(o[16 * h + 4 * k + 2]), __float_as_uint(o[16 * h + 4 * k + 3]));
+              transpose4(v);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (rr - q + k < rows)
+                  *reinterpret_cast<uint4*>(a.part_o + (prow - q + k) * S::DP + c * 32 + h * 16 + q * 4) = v[k];
+            }
           }
         }
         if (valid && whole && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-        if (valid && !whole) a.part_ml[(int64_t)piece * a.rows + r] = make_float2(m, l);
-        __syncwarp();
-        tc_fence_before();
+        if (valid && !whole) a.part_ml[prow] = make_float2(m, l);
       }
-      if (w.tb == 0 && w.te < w.T) {
-        open_b = w.b;
-        open_h = w.h;
-        open_m = w.m;
-        open_end = w.pos + w.T;
-      }
+      __syncwarp();
+      tc_fence_before();
+      if (w.tb == 0 && w.te < w.T)
+        open = Open{rows, (int)((w.pos + w.T - 1) / sy.start.share) - (int)blockIdx.x + 1, w.t0, w.h, w.m};
       __syncwarp();
       if (lane == 0) mbar_arrive(&sy.o_free[x]);
     }
-    if (threadIdx.x == 0)
-      a.open[blockIdx.x] = Open{ok && open_b >= 0, open_b, open_h, open_m, open_end, sy.start.share};
+    if (threadIdx.x == 0) {
+      if (!ok) open.rows = 0;
+      a.open[blockIdx.x] = open;
+    }
   } else if (warp < S::W_Q) {
     // ---------------------------------------------------------------- key and value loads
-    const int slot = warp - S::W_LOAD;
+    const int slot = (warp - S::W_LOAD) / S::LW, part = (warp - S::W_LOAD) % S::LW * (BN / S::LW);
     const uint32_t dst = smem_u32(ring + slot * S::SLOT);
     bool ok = true;
-    uint32_t e = 0, uses = 0;                         // ring entries so far; those of this slot
+    uint32_t e = slot, uses = 0;                      // this slot's next ring entry; its uses so far
+    uint32_t e0 = 0;                                  // the segment's first ring entry: tile tb's keys
     for (; w.more() && ok; w.next()) {
-      for (int t = w.tb; t < w.te && ok; ++t)
-        for (int kv = 0; kv < 2; ++kv, ++e) {
-          if ((int)(e % S::SL) != slot) continue;
-          if (!__all_sync(0xffffffffu, wait(&sy.empty[slot], (uses & 1) ^ 1, sy, a))) { ok = false; break; }
-          ++uses;
-          const int64_t j0 = (int64_t)t * BN;
-          const bool clean = kv && a.mask != DG_MASK_FULL && j0 + BN > w.clear();
-          load_rows<S, F8>(w, kv ? a.w.c.v : a.w.c.k, kv ? a.w.c.v_exp : a.w.c.k_exp, j0, dst, clean, sy);
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sy.full[slot]);
-        }
+      const uint32_t n = 2 * (uint32_t)(w.te - w.tb);
+      for (; e - e0 < n; e += S::SL) {
+        const bool kv = (e - e0) & 1;
+        const int64_t j0 = (int64_t)(w.tb + (int)((e - e0) >> 1)) * BN;
+        int row[BN / S::LW / 32];
+        find_rows<S>(w, j0 + part, row);              // under the wait for the slot
+        if (!__all_sync(0xffffffffu, wait(&sy.empty[slot], (uses & 1) ^ 1, sy, a))) { ok = false; break; }
+        ++uses;
+        const bool clean = kv && a.mask != DG_MASK_FULL && j0 + BN > w.clear();
+        load_rows<S>(w, kv ? a.w.c.v : a.w.c.k, kv ? a.w.c.v_exp : a.w.c.k_exp, row, part, dst, clean, sy);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sy.full[slot]);
+      }
+      e0 += n;
     }
   } else if (warp == S::W_Q) {
     // ---------------------------------------------------------------- queries
@@ -738,13 +904,17 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       const int c = lane % CPR;
       const int rows = w.rows();
       const uint32_t dst = smem_u32(smem);
+      const bool few = S::FEW && rows <= 32;
+#pragma unroll 8
       for (int r0 = 0; r0 < rows; r0 += RPI) {
         const int r = r0 + lane / CPR;
-        const int64_t rid = (int64_t)w.m * ROWS + (r < rows ? r : 0);
-        const int64_t i = rid / a.G, g = rid - i * a.G;
+        const uint32_t rid = (uint32_t)w.m * ROWS + (r < rows ? r : 0);
+        const uint32_t i = a.over_g(rid), g = rid - i * (uint32_t)a.G;
         const bool on = r < rows && c * 8 < D;
-        copy16(dst + (r >> 7) * S::QTILE + swizzled(r & 127, c, 128),
-               on ? a.q + (w.t0 + i) * a.q_ts + (w.h * a.G + g) * a.q_hs + c * 8 : a.q, on ? 16 : 0);
+        const __nv_bfloat16* src = on ? a.q + (int64_t)(w.t0 + i) * a.q_ts + (int64_t)(w.h * a.G + g) * a.q_hs + c * 8 : a.q;
+        copy16(dst + (r >> 7) * S::QTILE + swizzled(r & 127, c, 128), src, on ? 16 : 0);
+        if (few)
+          for (int k = 32; k < 128; k += 32) copy16(dst + swizzled(r + k, c, 128), src, on ? 16 : 0);
       }
       copies_landed();
       fence_async_shared();
@@ -843,36 +1013,61 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
   }
 }
 
-// Joins the pieces of the items that lie in more than one CTA's share: block
-// (c, y) those rows y, y + gridDim.y, ... of the item that CTA c began. Pieces
-// are added in the order of their keys by groups of warps, so that the result
-// does not depend on timing.
+// Joins the pieces of the items that lie in more than one CTA's share. The
+// rows of all such items form one list that the blocks take turns at; a row's
+// pieces are divided over 2, 4 or 8 warps and added in a fixed order, so that
+// the result does not depend on timing.
 template <class S>
-__global__ void __launch_bounds__(256) k_join(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(256) k_join(const __grid_constant__ Args a, int ctas) {
   constexpr int V = S::DP / 32;                       // columns per lane
   __shared__ float o_s[8][S::DP];
   __shared__ float m_s[8], l_s[8];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Open op = a.open[blockIdx.x];
-  if (!op.on) return;
+  __shared__ Open open_s[kMaxCtas];
+  __shared__ int upto[kMaxCtas + 1];                  // units before each item
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Walk<S::NT * 128, S::BN> w(a);
-  w.sequence(op.b);
-  w.h = op.h;
-  w.m = op.m;
-  const int rows = w.rows(), D = a.w.c.head_dim;
-  const int pieces = (int)((op.end - 1) / op.share) - (int)blockIdx.x + 1;
-  const int per = pieces > 4 ? 8 : pieces > 2 ? 4 : 2;   // warps per row
-  const int sub = warp % per;
-  for (int r0 = blockIdx.y * (8 / per); r0 < rows; r0 += gridDim.y * (8 / per)) {
-    const int r = r0 + warp / per;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (threadIdx.x < ctas) open_s[threadIdx.x] = a.open[threadIdx.x];
+  __syncthreads();
+  // warps per row, and units (groups of 8 / per rows) of an item
+  auto per_of = [](int pieces) { return pieces > 4 ? 8 : pieces > 2 ? 4 : 2; };
+  if (warp == 0) {
+    int run = 0;
+    for (int b0 = 0; b0 < ctas; b0 += 32) {
+      const int at = b0 + lane;
+      int u = 0;
+      if (at < ctas && open_s[at].rows) {
+        const int group = 8 / per_of(open_s[at].pieces);
+        u = (open_s[at].rows + group - 1) / group;
+      }
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, u, d);
+        if (lane >= d) u += o;
+      }
+      if (at < ctas) upto[at + 1] = run + u;
+      run += __shfl_sync(0xffffffffu, u, 31);
+    }
+    if (lane == 0) upto[0] = 0;
+  }
+  __syncthreads();
+  const int D = a.w.c.head_dim;
+  for (int unit = blockIdx.x; unit < upto[ctas]; unit += gridDim.x) {
+    int lo = 0, hi = ctas;                            // upto[lo] <= unit < upto[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (upto[mid] <= unit) lo = mid;
+      else hi = mid;
+    }
+    const Open& op = open_s[lo];
+    const int per = per_of(op.pieces), sub = warp % per;
+    const int r = (unit - upto[lo]) * (8 / per) + warp / per;
     float m = -INFINITY, l = 0.f, o[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) o[k] = 0.f;
-    if (r < rows) {
+    if (r < op.rows) {
 #pragma unroll 4
-      for (int p = sub; p < pieces; p += per) {
-        const int64_t at = (int64_t)((blockIdx.x + p) * 2 + (p == 0 ? 1 : 0)) * a.rows + r;
+      for (int p = sub; p < op.pieces; p += per) {
+        const int64_t at = (int64_t)((lo + p) * 2 + (p == 0 ? 1 : 0)) * a.rows + r;
         const float2 ml = a.part_ml[at];
         const float* src = a.part_o + at * S::DP + lane * V;
         float v[V];
@@ -883,8 +1078,8 @@ __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Args a) {
           v[k + 1] = f.y;
         }
         const float mn = fmaxf(m, ml.x);
-        const float sub_m = mn == -INFINITY ? 0.f : mn;
-        const float f0 = ex2(m - sub_m), f1 = ex2(ml.x - sub_m);
+        const float base = mn == -INFINITY ? 0.f : mn;
+        const float f0 = ex2(m - base), f1 = ex2(ml.x - base);
         l = l * f0 + ml.y * f1;
 #pragma unroll
         for (int k = 0; k < V; ++k) o[k] = o[k] * f0 + v[k] * f1;
@@ -895,20 +1090,20 @@ __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Args a) {
     for (int k = 0; k < V; ++k) o_s[warp][lane * V + k] = o[k];
     if (lane == 0) { m_s[warp] = m; l_s[warp] = l; }
     __syncthreads();
-    if (sub == 0 && r < rows) {
+    if (sub == 0 && r < op.rows) {
       for (int p = 1; p < per; ++p) {
         const float pm = m_s[warp + p], pl = l_s[warp + p];
         const float mn = fmaxf(m, pm);
-        const float sub_m = mn == -INFINITY ? 0.f : mn;
-        const float f0 = ex2(m - sub_m), f1 = ex2(pm - sub_m);
+        const float base = mn == -INFINITY ? 0.f : mn;
+        const float f0 = ex2(m - base), f1 = ex2(pm - base);
         l = l * f0 + pl * f1;
 #pragma unroll
         for (int k = 0; k < V; ++k) o[k] = o[k] * f0 + o_s[warp + p][lane * V + k] * f1;
         m = mn;
       }
-      const int64_t rid = (int64_t)w.m * (S::NT * 128) + r;
-      const int64_t i = rid / a.G, g = rid - i * a.G;
-      const int64_t orow = (w.t0 + i) * a.q_heads + w.h * a.G + g;
+      const uint32_t rid = (uint32_t)op.m * (S::NT * 128) + r;
+      const uint32_t i = a.over_g(rid), g = rid - i * (uint32_t)a.G;
+      const int64_t orow = (int64_t)(op.t0 + i) * a.q_heads + op.h * a.G + g;
       const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
 #pragma unroll
       for (int k = 0; k < V; k += 2)
@@ -947,23 +1142,25 @@ Plan make_plan(const dg_kv_cache& c, const dg_kv_batch& b, int q_heads) {
   return p;
 }
 
-template <class S, bool F8>
+template <class S>
 cudaError_t launch(const Args& a, int ctas, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(k_attend<S, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(k_attend<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
   if (e != cudaSuccess) return e;
-  k_attend<S, F8><<<ctas, S::THREADS, S::SMEM, s>>>(a);
+  k_attend<S><<<ctas, S::THREADS, S::SMEM, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || ctas == 1) return e;
   // the join's launch overlaps the kernel's end; it waits for it on the device
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas - 1, (unsigned)std::min(16, (a.rows + 7) / 8));
+  // a row per block at least, at most four blocks per SM: whatever the lengths,
+  // no more than ctas - 1 items are cut
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(4ll * ctas, (int64_t)(ctas - 1) * a.rows));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_join<S>, a);
+  return cudaLaunchKernelEx(&cfg, k_join<S>, a, ctas);
 }
 
 }  // namespace attn
@@ -987,6 +1184,10 @@ extern "C" size_t dg_cache_attention_scratch_bytes(const dg_kv_cache* cache, con
     fail(DG_EINVAL, "q_heads must be a multiple of kv_heads");
     return 0;
   }
+  if ((int64_t)batch->tokens * q_heads > (1 << 30)) {
+    fail(DG_EUNSUPPORTED, "tokens x q_heads must be at most 2^30");
+    return 0;
+  }
   return attn::make_plan(*cache, *batch, q_heads).total;
 }
 
@@ -1003,6 +1204,7 @@ extern "C" int dg_cache_attention(const dg_kv_cache* cache, const dg_kv_batch* b
   if (mask == DG_MASK_TREE && (mask_words < 0 || (mask_words && !tree_mask)))
     return fail(DG_EINVAL, "DG_MASK_TREE needs tree_mask and mask_words >= 0");
   if (batch->tokens == 0 || batch->batch == 0) return DG_OK;
+  if ((int64_t)batch->tokens * q_heads > (1 << 30)) return fail(DG_EUNSUPPORTED, "tokens x q_heads must be at most 2^30");
   if ((rc = kv_row_args(q, q_ts, q_hs))) return rc;
   if (!out || off16(out)) return fail(DG_EINVAL, "out must be 16-byte aligned and not NULL");
   if (!scratch || reinterpret_cast<uintptr_t>(scratch) % 256) return fail(DG_EINVAL, "scratch must be 256-byte aligned and not NULL");
@@ -1013,19 +1215,26 @@ extern "C" int dg_cache_attention(const dg_kv_cache* cache, const dg_kv_batch* b
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return kv_launched(e);
   char* sc = static_cast<char*>(scratch);
+  const uint32_t G = (uint32_t)(q_heads / cache->kv_heads);
+  int log = 0;                                     // r / G for r < 2^31: 2^log >= G, the multiplier rounded up
+  while ((1ll << log) < G) ++log;
+  const uint32_t mul = (uint32_t)(((1ull << (31 + log)) + G - 1) / G);
   const Args a{{*cache, *batch}, static_cast<const __nv_bfloat16*>(q), q_ts, q_hs, q_heads,
-               q_heads / cache->kv_heads, scale * 1.4426950408889634f, mask, tree_mask, mask_words,
+               (int)G, mul, 31 + log, scale * 1.4426950408889634f, mask, tree_mask, mask_words,
                static_cast<__nv_bfloat16*>(out), lse, reinterpret_cast<float*>(sc + p.o),
                reinterpret_cast<float2*>(sc + p.ml), reinterpret_cast<Open*>(sc + p.open), p.rows};
   const int ctas = std::min(sms, kMaxCtas);
   const bool f8 = cache->format == DG_KV_E4M3;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  auto go = [&](auto shape) {
-    using S = decltype(shape);
-    return f8 ? launch<S, true>(a, ctas, s) : launch<S, false>(a, ctas, s);
+  auto go = [&](auto dp, auto nt) {
+    constexpr int DP = decltype(dp)::value, NT = decltype(nt)::value;
+    return f8 ? launch<Shape<DP, NT, true>>(a, ctas, s) : launch<Shape<DP, NT, false>>(a, ctas, s);
   };
-  if (p.dp == 256) e = go(Shape<256, 1>());
-  else if (p.dp == 128) e = p.nt == 2 ? go(Shape<128, 2>()) : go(Shape<128, 1>());
-  else e = p.nt == 2 ? go(Shape<64, 2>()) : go(Shape<64, 1>());
+  using std::integral_constant;
+  const integral_constant<int, 1> one;
+  const integral_constant<int, 2> two;
+  if (p.dp == 256) e = go(integral_constant<int, 256>(), one);
+  else if (p.dp == 128) e = p.nt == 2 ? go(integral_constant<int, 128>(), two) : go(integral_constant<int, 128>(), one);
+  else e = p.nt == 2 ? go(integral_constant<int, 64>(), two) : go(integral_constant<int, 64>(), one);
   return kv_launched(e);
 }
