@@ -23,10 +23,11 @@
 // A CTA's warps:
 //   softmax   NT x 4 warps: TMEM lane = row; S from TMEM, P = 2^(t - m) back
 //             to TMEM as bf16, the running m and l in registers
-//   loads     SL warps, one per slot of the ring of key and value tiles: rows
-//             are gathered page by page (16-byte cp.async, or for e4m3 16-byte
-//             loads converted to bf16, which holds code x 2^e exactly) into
-//             the 128-byte swizzle that the MMA reads
+//   loads     one or two warps per slot of the ring of key and value tiles:
+//             runs of rows that lie together in a page by TMA, or single rows
+//             by 16-byte cp.async, into the 128-byte swizzle that the MMA
+//             reads; e4m3 codes are converted to bf16, which holds code x 2^e
+//             exactly
 //   queries   one warp: the item's query rows
 //   MMA       one thread: S = Q K^T (both from shared memory), O += P V (P from
 //             TMEM, V as it lies, keys along K), accumulators in TMEM
@@ -44,6 +45,7 @@
 #include "dg.h"
 #include "dg_cache.cuh"
 #include "dg_fp8.cuh"
+#include "dg_tc.h"
 #include "dg_tcgen05.cuh"
 
 namespace dg {
@@ -80,6 +82,7 @@ struct Args {
   float2* part_ml;             // [CTAs][2][rows] their m (log2 units) and l
   struct Open* open;           // [CTAs] the item a CTA begins and does not finish
   int rows;                    // rows kept per piece
+  int box;                     // rows per TMA copy: a power of two that divides page_size; 0: no TMA
 
   __device__ __forceinline__ uint32_t over_g(uint32_t r) const {
     return (uint32_t)(((uint64_t)r * g_mul) >> g_shift);
@@ -272,6 +275,7 @@ struct Sync {
   uint64_t s_full[2], p_full[2];   // S ready; P stored
   uint64_t o_done[2], o_free[2];   // P V done; O read
   uint64_t q_full, q_free, fin;
+  uint64_t raw[10];                // e4m3: a load warp's codes have landed
   uint64_t merge;                  // between the four warps that share a tile's rows
   uint32_t tmem;
   int abort, nonfinite;
@@ -394,6 +398,35 @@ __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t pair, float scale) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
   return pack_bf16(f.x * scale, f.y * scale);
 }
+// 16 codes, by their bits: the code's exponent and mantissa moved to where bf16
+// has them make code x 2^-120 (its subnormals bf16's own), and one product with
+// 2^(120 + e) makes the value; 52 integer and 8 packed instructions against 48
+// conversions, of which the hardware does a quarter as many per cycle. `pow`
+// is 2^(120 + e) twice, for e <= 7; beyond that, and where a code is NaN, the
+// conversions are taken.
+__device__ __forceinline__ void codes16_to_bf16(const uint4& v, uint32_t pow, float scale, bool large, uint32_t* o) {
+  const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+  uint32_t nan = 0;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    nan |= (x[t] & 0x7f7f7f7fu) + 0x01010101u;
+    const uint32_t hi = (x[t] & 0x80808080u) | ((x[t] >> 4) & 0x07070707u);
+    const uint32_t lo = (x[t] << 4) & 0xf0f0f0f0u;
+    const uint32_t a = __byte_perm(lo, hi, 0x5140), b = __byte_perm(lo, hi, 0x7362);
+    const __nv_bfloat162 p = *reinterpret_cast<const __nv_bfloat162*>(&pow);
+    const __nv_bfloat162 c = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), p);
+    const __nv_bfloat162 d = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), p);
+    o[2 * t] = *reinterpret_cast<const uint32_t*>(&c);
+    o[2 * t + 1] = *reinterpret_cast<const uint32_t*>(&d);
+  }
+  if (large || (nan & 0x80808080u)) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      o[2 * t] = codes_to_bf16(x[t], scale);
+      o[2 * t + 1] = codes_to_bf16(x[t] >> 16, scale);
+    }
+  }
+}
 
 // The cache rows of this warp's share of a key tile: rows lane, lane + 32, ...
 // of the BN / LW from position j0 on; -1 beyond the sequence or without a page.
@@ -408,23 +441,28 @@ __device__ __forceinline__ void find_rows(const W& w, int64_t j0, int* row) {
   }
 }
 
-// One warp fills its share of a ring slot (rows r0 to r0 + BN / LW) with key or
-// value rows. `clean`: the tile holds positions that a query row of the item
-// may not see; what is not finite there is replaced by zero and noted (0 x NaN
-// in the second product would reach every row).
+// Single rows. One warp copies its share of a ring slot (rows r0 to r0 + BN / LW;
+// zeros for a row of -1); e4m3 codes go where convert() takes them from.
 //
-// e4m3: the codes are copied into the upper half of the warp's part of the slot
-// and converted in place. In order of 64-column blocks and rows, 16 codes at
-// offset x of the codes become 32 bytes at offset 2x of the part, which holds
-// only codes already read; so the whole tile is in flight at once, without
+// e4m3: the codes lie in the upper half of the warp's part of the slot and are
+// converted in place. In order of 64-column blocks and rows, 16 codes at offset
+// x of the codes become 32 bytes at offset 2x of the part, which holds only
+// codes already read; so the whole tile is in flight at once, without
 // registers or a staging buffer.
-template <class S, typename W>
-__device__ __forceinline__ void load_rows(const W& w, const void* pages, const uint8_t* exps, const int* row,
-                                          int r0, uint32_t slot, bool clean, Sync& sy) {
+template <class S>
+struct Part {                                      // byte `lin` of the warp's part of a slot
+  static constexpr int RW = S::BN / S::LW, HALF = RW * 64, NB = S::DP / 64;
+  uint32_t slot;
+  int r0;
+  __device__ __forceinline__ uint32_t at(uint32_t lin) const {   // blocks of 2 HALF bytes, BN rows apart
+    return slot + lin / (2 * HALF) * (S::BN * 128) + r0 * 128 + lin % (2 * HALF);
+  }
+};
+
+template <class S>
+__device__ __forceinline__ void copy_rows(const Args& a, const void* pages, const int* row, int r0, uint32_t slot) {
   constexpr int RW = S::BN / S::LW;
-  const Args& a = w.a;
-  const int lane = threadIdx.x & 31;
-  const int D = a.w.c.head_dim;
+  const int lane = threadIdx.x & 31, D = a.w.c.head_dim;
   if constexpr (!S::F8) {
     constexpr int CPR = S::DP / 8, RPI = 32 / CPR; // chunks per row, rows per instruction
     const int c = lane % CPR;
@@ -437,74 +475,117 @@ __device__ __forceinline__ void load_rows(const W& w, const void* pages, const u
       const bool on = in && cr >= 0;
       copy16(slot + swizzled(r0 + r, c, S::BN), on ? base + (int64_t)cr * D : a.q, on ? 16 : 0);
     }
-    copies_landed();
-    if (clean) {
-      bool dirty = false;
-      for (int it = 0; it < RW / RPI; ++it) {
-        const uint32_t at = slot + swizzled(r0 + it * RPI + lane / CPR, c, S::BN);
-        const uint4 v = ld_shared(at);
-        const uint4 f = make_uint4(only_finite(v.x), only_finite(v.y), only_finite(v.z), only_finite(v.w));
-        if (f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w) {
-          st_shared(at, f);
-          dirty = true;
-        }
-      }
-      if (dirty) *(volatile int*)&sy.nonfinite = 1;
-    }
   } else {
-    constexpr int NB = S::DP / 64, HALF = RW * 64, PER = RW / 8, N = NB * PER, BATCH = 4;
+    using P = Part<S>;
+    const P part{slot, r0};
+    constexpr int PER = RW / 8;
     const int q = lane & 3, rl = lane >> 2;        // 16-code chunk of a block's row; row of 8
     const uint8_t* base = static_cast<const uint8_t*>(pages) + q * 16;
-    // byte `lin` of the warp's part: blocks of 2 HALF bytes, BN rows apart in the slot
-    auto part = [&](uint32_t lin) { return slot + lin / (2 * HALF) * (S::BN * 128) + r0 * 128 + lin % (2 * HALF); };
-    float scale[RW / 32];
 #pragma unroll
-    for (int p = 0; p < RW / 32; ++p)
-      scale[p] = row[p] >= 0 ? __uint_as_float(max(1u, min(254u, (uint32_t)__ldg(exps + row[p]))) << 23) : 0.f;
-#pragma unroll
-    for (int it = 0; it < N; ++it) {
+    for (int it = 0; it < P::NB * PER; ++it) {
       const int cb = it / PER, r = it % PER * 8 + rl;
       const int cr = __shfl_sync(0xffffffffu, row[it % PER * 8 / 32], r & 31);
       const bool on = cr >= 0 && cb * 64 + q * 16 < D;
-      copy16(part(NB * HALF + cb * HALF + it % PER * 512) + lane * 16, on ? base + (int64_t)cr * D + cb * 64 : (const void*)a.q,
+      copy16(part.at(P::NB * P::HALF + it * 512) + lane * 16, on ? base + (int64_t)cr * D + cb * 64 : (const void*)a.q,
              on ? 16 : 0);
     }
-    copies_landed();
+  }
+  copies_landed();
+  __syncwarp();
+}
+
+// A run of rows at a time: the lanes' TMA copies of the warp's share, counted on
+// `bar`. Every row has a page, so that only the first of each run is looked up.
+template <class S>
+__device__ __forceinline__ void copy_boxes(const Args& a, const CUtensorMap* map, const int* row, int r0, uint32_t slot,
+                                           uint64_t* bar) {
+  using P = Part<S>;
+  const int lane = threadIdx.x & 31;
+  const int run = lane / P::NB * a.box, cb = lane % P::NB;      // the lane's rows and 64-column block
+  int first = 0;
+#pragma unroll
+  for (int p = 0; p < P::RW / 32; ++p) {
+    const int t = __shfl_sync(0xffffffffu, row[p], run & 31);
+    if (run >> 5 == p) first = t;
+  }
+  fence_async_shared();                            // after the slot's earlier ordinary writes
+  if (lane == 0) mbar_expect_tx(bar, P::NB * P::HALF * (S::F8 ? 1 : 2));
+  __syncwarp();
+  if (run >= P::RW) return;
+  const uint32_t dst = S::F8 ? Part<S>{slot, r0}.at(P::NB * P::HALF + cb * P::HALF + run * 64)
+                             : slot + cb * (S::BN * 128) + run * 128;
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(cb * 64), "r"(first)
+      : "memory");
+}
+
+// The exponents of the warp's rows (127 for a row of -1).
+template <class S>
+__device__ __forceinline__ void find_exps(const uint8_t* exps, const int* row, int* e) {
+#pragma unroll
+  for (int p = 0; p < S::BN / S::LW / 32; ++p)
+    e[p] = row[p] >= 0 ? max(1, min(254, (int)__ldg(exps + row[p]))) : 127;
+}
+
+// e4m3: the warp's codes to bf16, in place. `clean`: as in clean_rows.
+template <class S>
+__device__ __forceinline__ void convert(const int* exps, int r0, uint32_t slot, bool clean, Sync& sy) {
+  using P = Part<S>;
+  constexpr int PER = P::RW / 8, N = P::NB * PER, BATCH = 4;
+  const P part{slot, r0};
+  const int lane = threadIdx.x & 31, q = lane & 3, rl = lane >> 2;
+  bool large = false;
+#pragma unroll
+  for (int p = 0; p < P::RW / 32; ++p) large |= exps[p] > 134;
+  large = __any_sync(0xffffffffu, large);
+#pragma unroll
+  for (int i0 = 0; i0 < N; i0 += BATCH) {
+    uint4 v[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) v[k] = ld_shared(part.at(P::NB * P::HALF + (i0 + k) * 512) + lane * 16);
     __syncwarp();
 #pragma unroll
-    for (int i0 = 0; i0 < N; i0 += BATCH) {
-      uint4 v[BATCH];
+    for (int k = 0; k < BATCH; ++k) {
+      const int cb = (i0 + k) / PER, r = (i0 + k) % PER * 8 + rl;
+      const uint32_t e = __shfl_sync(0xffffffffu, exps[(i0 + k) % PER * 8 / 32], r & 31);
+      uint32_t o[8];
+      codes16_to_bf16(v[k], min(e + 120, 254u) * 0x00800080u, __uint_as_float(e << 23), large, o);
+      if (clean) {
+        bool dirty = false;
 #pragma unroll
-      for (int k = 0; k < BATCH; ++k)
-        v[k] = ld_shared(part(NB * HALF + (i0 + k) / PER * HALF + (i0 + k) % PER * 512) + lane * 16);
-      __syncwarp();
-#pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
-        const int cb = (i0 + k) / PER, r = (i0 + k) % PER * 8 + rl;
-        const float f = __shfl_sync(0xffffffffu, scale[(i0 + k) % PER * 8 / 32], r & 31);
-        const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-        uint32_t o[8];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          o[2 * t] = codes_to_bf16(x[t], f);
-          o[2 * t + 1] = codes_to_bf16(x[t] >> 16, f);
+        for (int t = 0; t < 8; ++t) {
+          const uint32_t g = only_finite(o[t]);
+          dirty |= g != o[t];
+          o[t] = g;
         }
-        if (clean) {
-          bool dirty = false;
-#pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            const uint32_t g = only_finite(o[t]);
-            dirty |= g != o[t];
-            o[t] = g;
-          }
-          if (dirty) *(volatile int*)&sy.nonfinite = 1;
-        }
-        st_shared(slot + swizzled(r0 + r, cb * 8 + 2 * q, S::BN), make_uint4(o[0], o[1], o[2], o[3]));
-        st_shared(slot + swizzled(r0 + r, cb * 8 + 2 * q + 1, S::BN), make_uint4(o[4], o[5], o[6], o[7]));
+        if (dirty) *(volatile int*)&sy.nonfinite = 1;
       }
-      __syncwarp();
+      st_shared(slot + swizzled(r0 + r, cb * 8 + 2 * q, S::BN), make_uint4(o[0], o[1], o[2], o[3]));
+      st_shared(slot + swizzled(r0 + r, cb * 8 + 2 * q + 1, S::BN), make_uint4(o[4], o[5], o[6], o[7]));
+    }
+    __syncwarp();
+  }
+}
+
+// bf16: what is not finite in the warp's rows replaced by zero and noted. For
+// value tiles that hold positions which a query row of the item may not see:
+// 0 x NaN in the second product would reach every row.
+template <class S>
+__device__ __forceinline__ void clean_rows(uint32_t slot, Sync& sy) {
+  constexpr int CPR = S::DP / 8, RPI = 32 / CPR;
+  const int lane = threadIdx.x & 31, c = lane % CPR;
+  bool dirty = false;
+  for (int it = 0; it < S::BN / RPI; ++it) {
+    const uint32_t at = slot + swizzled(it * RPI + lane / CPR, c, S::BN);
+    const uint4 v = ld_shared(at);
+    const uint4 f = make_uint4(only_finite(v.x), only_finite(v.y), only_finite(v.z), only_finite(v.w));
+    if (f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w) {
+      st_shared(at, f);
+      dirty = true;
     }
   }
+  if (dirty) *(volatile int*)&sy.nonfinite = 1;
 }
 
 // o (columns d .. d + 3 of a row's sum) with the infinities and NaN among the
@@ -571,13 +652,14 @@ __device__ __forceinline__ void transpose4(uint4* v) {
 // quarter of the keys, with an m and l of its own. The four are joined at the
 // end of the item.
 template <class S>
-__global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap k_map,
+                                                           const __grid_constant__ CUtensorMap v_map) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* ring = smem + S::NT * S::QTILE;
   Sync& sy = *reinterpret_cast<Sync*>(ring + S::SL * S::SLOT);
-  static_assert(sizeof(Sync) <= 512, "barriers");
+  static_assert(sizeof(Sync) <= 512 && S::SL <= 8 && (!S::F8 || S::SL * S::LW <= 10), "barriers");
   float* few_o = reinterpret_cast<float*>(ring + S::SL * S::SLOT + 512);         // [4][32][16]
   float2* few_ml = reinterpret_cast<float2*>(few_o + 4 * 32 * 16);              // [4][32]
   int64_t* pref = reinterpret_cast<int64_t*>(ring);
@@ -596,6 +678,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     mbar_init(&sy.q_free, 1);
     mbar_init(&sy.fin, 1);
     mbar_init(&sy.merge, 4);
+    for (int x = 0; x < S::SL * S::LW && S::F8; ++x) mbar_init(&sy.raw[x], 1);
     sy.abort = 0;
     sy.nonfinite = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -874,25 +957,51 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     const int slot = (warp - S::W_LOAD) / S::LW, part = (warp - S::W_LOAD) % S::LW * (BN / S::LW);
     const uint32_t dst = smem_u32(ring + slot * S::SLOT);
     bool ok = true;
-    uint32_t e = slot, uses = 0;                      // this slot's next ring entry; its uses so far
+    uint32_t e = slot, uses = 0, raws = 0;            // this slot's next ring entry; its uses so far, by TMA
+    uint64_t* landing = nullptr;                      // where the last TMA copies arrive, and in which phase
+    uint32_t landed = 0;
     uint32_t e0 = 0;                                  // the segment's first ring entry: tile tb's keys
     for (; w.more() && ok; w.next()) {
       const uint32_t n = 2 * (uint32_t)(w.te - w.tb);
       for (; e - e0 < n; e += S::SL) {
         const bool kv = (e - e0) & 1;
         const int64_t j0 = (int64_t)(w.tb + (int)((e - e0) >> 1)) * BN;
-        int row[BN / S::LW / 32];
+        int row[BN / S::LW / 32], exps[BN / S::LW / 32];
         find_rows<S>(w, j0 + part, row);              // under the wait for the slot
+        if (S::F8) find_exps<S>(kv ? a.w.c.v_exp : a.w.c.k_exp, row, exps);
+        const bool clean = kv && a.mask != DG_MASK_FULL && j0 + BN > w.clear();
+        // by TMA unless a row is to be left out or looked through
+        bool boxes = a.box && !clean;
+#pragma unroll
+        for (int p = 0; p < BN / S::LW / 32; ++p) boxes = boxes && row[p] >= 0;
+        boxes = __all_sync(0xffffffffu, boxes);
         if (!__all_sync(0xffffffffu, wait(&sy.empty[slot], (uses & 1) ^ 1, sy, a))) { ok = false; break; }
         ++uses;
-        const bool clean = kv && a.mask != DG_MASK_FULL && j0 + BN > w.clear();
-        load_rows<S>(w, kv ? a.w.c.v : a.w.c.k, kv ? a.w.c.v_exp : a.w.c.k_exp, row, part, dst, clean, sy);
+        if (boxes) {
+          uint64_t* bar = S::F8 ? &sy.raw[warp - S::W_LOAD] : &sy.full[slot];
+          copy_boxes<S>(a, kv ? &v_map : &k_map, row, part, dst, bar);
+          landing = bar;
+          landed = (S::F8 ? raws : uses - 1) & 1;
+          if constexpr (S::F8) {
+            if (!__all_sync(0xffffffffu, wait(bar, raws & 1, sy, a))) { ok = false; break; }
+            ++raws;
+          } else {
+            continue;                                 // the copies arrive on `full` themselves
+          }
+        } else {
+          copy_rows<S>(a, kv ? a.w.c.v : a.w.c.k, row, part, dst);
+          landing = nullptr;
+        }
+        if constexpr (S::F8) convert<S>(exps, part, dst, clean, sy);
+        else if (clean) clean_rows<S>(dst, sy);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sy.full[slot]);
       }
       e0 += n;
     }
+    // a CTA that gives up still waits for its last copies
+    if (landing) wait(landing, landed, sy, a, false);
   } else if (warp == S::W_Q) {
     // ---------------------------------------------------------------- queries
     bool ok = true;
@@ -1143,10 +1252,20 @@ Plan make_plan(const dg_kv_cache& c, const dg_kv_batch& b, int q_heads) {
 }
 
 template <class S>
-cudaError_t launch(const Args& a, int ctas, cudaStream_t s) {
+cudaError_t launch(Args a, int ctas, cudaStream_t s) {
+  // TMA copies take runs of rows that lie together: a power of two that divides
+  // page_size, at least 8 (one swizzle pattern) and at most a warp's share
+  const dg_kv_cache& c = a.w.c;
+  a.box = std::min(c.page_size & -c.page_size, S::BN / S::LW);
+  if (a.box < 8 || c.head_dim < 64 || c.pages == 0) a.box = 0;
+  alignas(64) CUtensorMap maps[2] = {};
+  const uint64_t rows = (uint64_t)c.pages * c.kv_heads * c.page_size;
+  if (a.box && (!tc_encode_2d_rows(&maps[0], c.k, c.head_dim, rows, 64, a.box, S::F8) ||
+                !tc_encode_2d_rows(&maps[1], c.v, c.head_dim, rows, 64, a.box, S::F8)))
+    return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(k_attend<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
   if (e != cudaSuccess) return e;
-  k_attend<S><<<ctas, S::THREADS, S::SMEM, s>>>(a);
+  k_attend<S><<<ctas, S::THREADS, S::SMEM, s>>>(a, maps[0], maps[1]);
   if ((e = cudaGetLastError()) != cudaSuccess || ctas == 1) return e;
   // the join's launch overlaps the kernel's end; it waits for it on the device
   cudaLaunchAttribute at[1];
@@ -1222,7 +1341,7 @@ extern "C" int dg_cache_attention(const dg_kv_cache* cache, const dg_kv_batch* b
   const Args a{{*cache, *batch}, static_cast<const __nv_bfloat16*>(q), q_ts, q_hs, q_heads,
                (int)G, mul, 31 + log, scale * 1.4426950408889634f, mask, tree_mask, mask_words,
                static_cast<__nv_bfloat16*>(out), lse, reinterpret_cast<float*>(sc + p.o),
-               reinterpret_cast<float2*>(sc + p.ml), reinterpret_cast<Open*>(sc + p.open), p.rows};
+               reinterpret_cast<float2*>(sc + p.ml), reinterpret_cast<Open*>(sc + p.open), p.rows, 0};
   const int ctas = std::min(sms, kMaxCtas);
   const bool f8 = cache->format == DG_KV_E4M3;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -33,6 +33,10 @@ bool tc_supported(int C, int V, int d);
 // [outer][inner] array, box [box_outer][box_inner], 128-byte swizzle.
 bool tc_encode_2d_bf16(void* map, const void* base, uint64_t inner, uint64_t outer,
                        uint32_t box_inner, uint32_t box_outer);
+// The same over rows of bf16 (128-byte swizzle) or of bytes (as they lie), for
+// the cache's pages.
+bool tc_encode_2d_rows(void* map, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
+                       uint32_t box_outer, bool bytes);
 // tc_supported, and the current device has SMs enough for both CTA roles.
 bool tc_fits_device(int C, int V, int d);
 // The work split tc_layout picks on a GPU with `sms` SMs, in the order
