@@ -13,9 +13,10 @@
 // one TMEM lane each); an item is NT tiles of one sequence and head.
 //
 // Work split. An item's keys come in tiles of BN. All items' key tiles, in
-// order (sequence, head, item), form one list, and CTA c of a persistent grid
-// takes a contiguous share of it: whatever the batch's lengths, every SM has
-// the same number of key tiles and there is one wave. A share may begin or end
+// order (sequence, head, item), form one list, with kItem empty places before
+// each item that stand for its queries, first products and result; CTA c of a
+// persistent grid takes a contiguous share of it: whatever the batch's lengths,
+// every SM has the same work and there is one wave. A share may begin or end
 // inside an item; such pieces go to scratch with their m and l, and a second
 // launch joins them in the order of the list. Lengths are read on the device,
 // so a captured graph follows them.
@@ -28,7 +29,8 @@
 //             by 16-byte cp.async, into the 128-byte swizzle that the MMA
 //             reads; e4m3 codes are converted to bf16, which holds code x 2^e
 //             exactly
-//   queries   one warp: the item's query rows
+//             exactly. Each also brings its share of an item's query rows,
+//             after its first tile of the item
 //   MMA       one thread: S = Q K^T (both from shared memory), O += P V (P from
 //             TMEM, V as it lies, keys along K), accumulators in TMEM
 // With NT = 2 the two tiles share each key and value tile and alternate, so
@@ -60,6 +62,7 @@ using namespace tc;
 
 constexpr int kMaxCtas = 148;                 // scratch is laid out for at most this many
 constexpr int TMEM_COLS = 512;
+constexpr int kItem = 3;                      // an item's cost beside its key tiles, in key tiles
 constexpr float kGrow = 8.0f;                 // log2 growth of a maximum that rescales O
 constexpr unsigned long long kWaitNs = 2000000000ull;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -109,7 +112,7 @@ struct Shape {
   static constexpr bool FEW = NT == 1 && BN == 128;
   static constexpr int SLOT = BN * DP * 2;
   static constexpr int QTILE = 128 * DP * 2;
-  static constexpr int W_LOAD = NT * 4, W_Q = W_LOAD + SL * LW, W_MMA = W_Q + 1;
+  static constexpr int W_LOAD = NT * 4, N_LOAD = SL * LW, W_MMA = W_LOAD + N_LOAD;
   static constexpr int THREADS = (W_MMA + 1) * 32;
   static constexpr int T_S = NT == 2 ? 128 : BN;       // TMEM columns between S buffers
   static constexpr int T_O = NT == 2 ? 256 : 2 * BN;   // first column of O
@@ -128,7 +131,7 @@ struct Walk {
   int b, h, m;                 // sequence, key/value head, item of the pair
   int n, past, t0;             // the sequence's new tokens, cached positions, first row
   int tb, te, T;               // this segment's key tiles [tb, te) of the item's T
-  int64_t pos, hi;             // position in the list, end of the CTA's share
+  int64_t at, lo, hi;          // the item's first place in the list; the CTA's share
 
   __device__ __forceinline__ Walk(const Args& a_) : a(a_) {}
   __device__ __forceinline__ void sequence(int b_) {
@@ -150,10 +153,18 @@ struct Walk {
   __device__ __forceinline__ int64_t clear() const {
     return a.mask == DG_MASK_FULL ? keys() : a.mask == DG_MASK_TREE ? past : (int64_t)past + a.over_g((uint32_t)m * ROWS) + 1;
   }
-  __device__ __forceinline__ bool more() const { return pos < hi; }
+  // (A share that ends within an item's empty places leaves the item alone.)
+  __device__ __forceinline__ bool more() const { return te > tb; }
+  __device__ __forceinline__ void segment() {
+    T = tiles(m);
+    const int64_t first = at + kItem;
+    tb = lo > first ? (int)(lo - first) : 0;
+    te = hi - first < T ? (int)(hi - first) : T;
+  }
   __device__ __forceinline__ void next() {
-    pos += te - tb;
-    if (pos >= hi) return;
+    at += kItem + T;
+    te = tb;
+    if (at >= hi) return;
     if (++m == items()) {
       m = 0;
       if (++h == a.w.c.kv_heads) {
@@ -161,9 +172,7 @@ struct Walk {
         do { sequence(b + 1); } while (n == 0);       // the list ends before the batch does
       }
     }
-    T = tiles(m);
-    tb = 0;
-    te = (int)(T < hi - pos ? T : hi - pos);
+    segment();
   }
   __device__ __forceinline__ int rows() const {
     return min(n * a.G - m * ROWS, ROWS);
@@ -172,8 +181,8 @@ struct Walk {
 
 // Where a CTA's share begins; worked out once per CTA.
 struct Start {
-  int64_t lo, hi, share;
-  int b, h, m, tb;
+  int64_t lo, hi, share, at;
+  int b, h, m;
 };
 
 // The whole CTA: tiles per head of every sequence, their prefix sums (in
@@ -187,9 +196,9 @@ __device__ __forceinline__ void plan(const Args& a, int64_t* pref, Start* st) {
     w.sequence(b);
     const int it = w.items();
     int64_t u = 0;
-    if (a.mask != DG_MASK_CAUSAL) u = it ? (int64_t)it * w.tiles(0) : 0;
+    if (a.mask != DG_MASK_CAUSAL) u = it ? (int64_t)it * (w.tiles(0) + kItem) : 0;
     else if (it > kAlone) u = -1;
-    else for (int x = 0; x < it; ++x) u += w.tiles(x);
+    else for (int x = 0; x < it; ++x) u += w.tiles(x) + kItem;
     pref[b + 1] = u;
   }
   __syncthreads();
@@ -198,7 +207,7 @@ __device__ __forceinline__ void plan(const Args& a, int64_t* pref, Start* st) {
     if (pref[b + 1] >= 0) continue;
     w.sequence(b);
     int64_t u = 0;
-    for (int x = lane, it = w.items(); x < it; x += 32) u += w.tiles(x);
+    for (int x = lane, it = w.items(); x < it; x += 32) u += w.tiles(x) + kItem;
 #pragma unroll
     for (int d = 16; d; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
     __syncwarp();
@@ -241,13 +250,13 @@ __device__ __forceinline__ void plan(const Args& a, int64_t* pref, Start* st) {
         rest -= st->h * per;
         int x = 0;
         if (a.mask != DG_MASK_CAUSAL) {
-          x = (int)(rest / w.tiles(0));
-          rest -= (int64_t)x * w.tiles(0);
+          x = (int)(rest / (w.tiles(0) + kItem));
+          rest -= (int64_t)x * (w.tiles(0) + kItem);
         } else {
-          for (int t; rest >= (t = w.tiles(x)); ++x) rest -= t;
+          for (int t; rest >= (t = w.tiles(x) + kItem); ++x) rest -= t;
         }
         st->m = x;
-        st->tb = (int)rest;
+        st->at = st->lo - rest;
       }
     }
   }
@@ -256,15 +265,15 @@ __device__ __forceinline__ void plan(const Args& a, int64_t* pref, Start* st) {
 
 template <int ROWS, int BN>
 __device__ __forceinline__ void begin(Walk<ROWS, BN>& w, const Start& st) {
-  w.pos = st.lo;
+  w.lo = st.lo;
   w.hi = st.hi;
-  if (w.pos >= w.hi) return;
+  w.tb = w.te = 0;
+  if (st.lo >= st.hi) return;
   w.sequence(st.b);
   w.h = st.h;
   w.m = st.m;
-  w.T = w.tiles(w.m);
-  w.tb = st.tb;
-  w.te = (int)(w.T - w.tb < w.hi - w.pos ? w.T : w.tb + (w.hi - w.pos));
+  w.at = st.at;
+  w.segment();
 }
 
 // ---------------------------------------------------------------------------
@@ -463,31 +472,43 @@ template <class S>
 __device__ __forceinline__ void copy_rows(const Args& a, const void* pages, const int* row, int r0, uint32_t slot) {
   constexpr int RW = S::BN / S::LW;
   const int lane = threadIdx.x & 31, D = a.w.c.head_dim;
+  auto pick = [&](int p) {                         // row[p], by selects
+    int x = row[0];
+#pragma unroll
+    for (int t = 1; t < RW / 32; ++t) x = p == t ? row[t] : x;
+    return x;
+  };
   if constexpr (!S::F8) {
     constexpr int CPR = S::DP / 8, RPI = 32 / CPR; // chunks per row, rows per instruction
     const int c = lane % CPR;
     const bool in = c * 8 < D;
     const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(pages) + c * 8;
-#pragma unroll
-    for (int it = 0; it < RW / RPI; ++it) {
-      const int r = it * RPI + lane / CPR;
-      const int cr = __shfl_sync(0xffffffffu, row[it * RPI / 32], r & 31);
-      const bool on = in && cr >= 0;
-      copy16(slot + swizzled(r0 + r, c, S::BN), on ? base + (int64_t)cr * D : a.q, on ? 16 : 0);
+#pragma unroll 1
+    for (int p = 0; p < RW / 32; ++p) {
+      const int mine = pick(p);
+#pragma unroll 8
+      for (int it = 0; it < 32 / RPI; ++it) {
+        const int r = it * RPI + lane / CPR;
+        const int cr = __shfl_sync(0xffffffffu, mine, r);
+        const bool on = in && cr >= 0;
+        copy16(slot + swizzled(r0 + p * 32 + r, c, S::BN), on ? base + (int64_t)cr * D : a.q, on ? 16 : 0);
+      }
     }
   } else {
     using P = Part<S>;
     const P part{slot, r0};
-    constexpr int PER = RW / 8;
     const int q = lane & 3, rl = lane >> 2;        // 16-code chunk of a block's row; row of 8
     const uint8_t* base = static_cast<const uint8_t*>(pages) + q * 16;
+#pragma unroll 1
+    for (int n = 0; n < P::NB * (RW / 32); ++n) {
+      const int cb = n / (RW / 32), mine = pick(n % (RW / 32));
 #pragma unroll
-    for (int it = 0; it < P::NB * PER; ++it) {
-      const int cb = it / PER, r = it % PER * 8 + rl;
-      const int cr = __shfl_sync(0xffffffffu, row[it % PER * 8 / 32], r & 31);
-      const bool on = cr >= 0 && cb * 64 + q * 16 < D;
-      copy16(part.at(P::NB * P::HALF + it * 512) + lane * 16, on ? base + (int64_t)cr * D + cb * 64 : (const void*)a.q,
-             on ? 16 : 0);
+      for (int k = 0; k < 4; ++k) {
+        const int cr = __shfl_sync(0xffffffffu, mine, k * 8 + rl);
+        const bool on = cr >= 0 && cb * 64 + q * 16 < D;
+        copy16(part.at(P::NB * P::HALF + n * 2048) + k * 512 + lane * 16,
+               on ? base + (int64_t)cr * D + cb * 64 : (const void*)a.q, on ? 16 : 0);
+      }
     }
   }
   copies_landed();
@@ -520,6 +541,27 @@ __device__ __forceinline__ void copy_boxes(const Args& a, const CUtensorMap* map
       : "memory");
 }
 
+// Warp `part` of N_LOAD brings its share of the item's query rows.
+template <class S, typename W>
+__device__ __forceinline__ void load_queries(const W& w, int part, uint32_t dst) {
+  constexpr int CPR = S::DP / 8, RPI = 32 / CPR, ROWS = S::NT * 128;
+  const Args& a = w.a;
+  const int lane = threadIdx.x & 31, c = lane % CPR, rows = w.rows();
+  const bool few = S::FEW && rows <= 32;
+#pragma unroll 4
+  for (int r0 = part * RPI; r0 < rows; r0 += S::N_LOAD * RPI) {
+    const int r = r0 + lane / CPR;
+    const uint32_t rid = (uint32_t)w.m * ROWS + (r < rows ? r : 0);
+    const uint32_t i = a.over_g(rid), g = rid - i * (uint32_t)a.G;
+    const bool on = r < rows && c * 8 < a.w.c.head_dim;
+    const __nv_bfloat16* src = on ? a.q + (int64_t)(w.t0 + i) * a.q_ts + (int64_t)(w.h * a.G + g) * a.q_hs + c * 8 : a.q;
+    copy16(dst + (r >> 7) * S::QTILE + swizzled(r & 127, c, 128), src, on ? 16 : 0);
+    if (few)
+      for (int k = 32; k < 128; k += 32) copy16(dst + swizzled(r + k, c, 128), src, on ? 16 : 0);
+  }
+  copies_landed();
+}
+
 // The exponents of the warp's rows (127 for a row of -1).
 template <class S>
 __device__ __forceinline__ void find_exps(const uint8_t* exps, const int* row, int* e) {
@@ -532,23 +574,29 @@ __device__ __forceinline__ void find_exps(const uint8_t* exps, const int* row, i
 template <class S>
 __device__ __forceinline__ void convert(const int* exps, int r0, uint32_t slot, bool clean, Sync& sy) {
   using P = Part<S>;
-  constexpr int PER = P::RW / 8, N = P::NB * PER, BATCH = 4;
+  constexpr int G32 = P::RW / 32;                     // groups of 32 rows
   const P part{slot, r0};
   const int lane = threadIdx.x & 31, q = lane & 3, rl = lane >> 2;
   bool large = false;
 #pragma unroll
-  for (int p = 0; p < P::RW / 32; ++p) large |= exps[p] > 134;
+  for (int p = 0; p < G32; ++p) large |= exps[p] > 134;
   large = __any_sync(0xffffffffu, large);
+  // 64 columns of 32 rows at a time. The loop stays a loop: unrolled, its code
+  // streamed through the instruction cache and took four times as long.
+#pragma unroll 1
+  for (int n = 0; n < P::NB * G32; ++n) {
+    const int cb = n / G32, p = n % G32;
+    int ee = exps[0];
 #pragma unroll
-  for (int i0 = 0; i0 < N; i0 += BATCH) {
-    uint4 v[BATCH];
+    for (int t = 1; t < G32; ++t) ee = p == t ? exps[t] : ee;
+    uint4 v[4];
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) v[k] = ld_shared(part.at(P::NB * P::HALF + (i0 + k) * 512) + lane * 16);
+    for (int k = 0; k < 4; ++k) v[k] = ld_shared(part.at(P::NB * P::HALF + n * 2048) + k * 512 + lane * 16);
     __syncwarp();
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      const int cb = (i0 + k) / PER, r = (i0 + k) % PER * 8 + rl;
-      const uint32_t e = __shfl_sync(0xffffffffu, exps[(i0 + k) % PER * 8 / 32], r & 31);
+    for (int k = 0; k < 4; ++k) {
+      const int r = r0 + p * 32 + k * 8 + rl;
+      const uint32_t e = __shfl_sync(0xffffffffu, ee, k * 8 + rl);
       uint32_t o[8];
       codes16_to_bf16(v[k], min(e + 120, 254u) * 0x00800080u, __uint_as_float(e << 23), large, o);
       if (clean) {
@@ -561,8 +609,8 @@ __device__ __forceinline__ void convert(const int* exps, int r0, uint32_t slot, 
         }
         if (dirty) *(volatile int*)&sy.nonfinite = 1;
       }
-      st_shared(slot + swizzled(r0 + r, cb * 8 + 2 * q, S::BN), make_uint4(o[0], o[1], o[2], o[3]));
-      st_shared(slot + swizzled(r0 + r, cb * 8 + 2 * q + 1, S::BN), make_uint4(o[4], o[5], o[6], o[7]));
+      st_shared(slot + swizzled(r, cb * 8 + 2 * q, S::BN), make_uint4(o[0], o[1], o[2], o[3]));
+      st_shared(slot + swizzled(r, cb * 8 + 2 * q + 1, S::BN), make_uint4(o[4], o[5], o[6], o[7]));
     }
     __syncwarp();
   }
@@ -674,7 +722,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       mbar_init(&sy.o_done[x], 1);
       mbar_init(&sy.o_free[x], 4);
     }
-    mbar_init(&sy.q_full, 1);
+    mbar_init(&sy.q_full, S::N_LOAD);
     mbar_init(&sy.q_free, 1);
     mbar_init(&sy.fin, 1);
     mbar_init(&sy.merge, 4);
@@ -944,7 +992,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       __syncwarp();
       tc_fence_before();
       if (w.tb == 0 && w.te < w.T)
-        open = Open{rows, (int)((w.pos + w.T - 1) / sy.start.share) - (int)blockIdx.x + 1, w.t0, w.h, w.m};
+        open = Open{rows, (int)((w.at + kItem + w.T - 1) / sy.start.share) - (int)blockIdx.x + 1, w.t0, w.h, w.m};
       __syncwarp();
       if (lane == 0) mbar_arrive(&sy.o_free[x]);
     }
@@ -952,7 +1000,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       if (!ok) open.rows = 0;
       a.open[blockIdx.x] = open;
     }
-  } else if (warp < S::W_Q) {
+  } else if (warp < S::W_MMA) {
     // ---------------------------------------------------------------- key and value loads
     const int slot = (warp - S::W_LOAD) / S::LW, part = (warp - S::W_LOAD) % S::LW * (BN / S::LW);
     const uint32_t dst = smem_u32(ring + slot * S::SLOT);
@@ -961,9 +1009,21 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     uint64_t* landing = nullptr;                      // where the last TMA copies arrive, and in which phase
     uint32_t landed = 0;
     uint32_t e0 = 0;                                  // the segment's first ring entry: tile tb's keys
-    for (; w.more() && ok; w.next()) {
+    uint32_t seg = 0;
+    for (; w.more() && ok; w.next(), ++seg) {
       const uint32_t n = 2 * (uint32_t)(w.te - w.tb);
-      for (; e - e0 < n; e += S::SL) {
+      bool q_due = true;
+      for (;; e += S::SL) {
+        if (q_due && (e - e0 >= n || e >= e0 + S::SL)) {
+          q_due = false;
+          if (seg && !__all_sync(0xffffffffu, wait(&sy.q_free, (seg - 1) & 1, sy, a))) { ok = false; break; }
+          load_queries<S>(w, warp - S::W_LOAD, smem_u32(smem));
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sy.q_full);
+        }
+        if (e - e0 >= n) break;
+
         const bool kv = (e - e0) & 1;
         const int64_t j0 = (int64_t)(w.tb + (int)((e - e0) >> 1)) * BN;
         int row[BN / S::LW / 32], exps[BN / S::LW / 32];
@@ -1002,34 +1062,6 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     }
     // a CTA that gives up still waits for its last copies
     if (landing) wait(landing, landed, sy, a, false);
-  } else if (warp == S::W_Q) {
-    // ---------------------------------------------------------------- queries
-    bool ok = true;
-    uint32_t seg = 0;
-    const int D = a.w.c.head_dim;
-    for (; w.more() && ok; w.next(), ++seg) {
-      if (seg && !__all_sync(0xffffffffu, wait(&sy.q_free, (seg - 1) & 1, sy, a))) { ok = false; break; }
-      constexpr int CPR = S::DP / 8, RPI = 32 / CPR;
-      const int c = lane % CPR;
-      const int rows = w.rows();
-      const uint32_t dst = smem_u32(smem);
-      const bool few = S::FEW && rows <= 32;
-#pragma unroll 8
-      for (int r0 = 0; r0 < rows; r0 += RPI) {
-        const int r = r0 + lane / CPR;
-        const uint32_t rid = (uint32_t)w.m * ROWS + (r < rows ? r : 0);
-        const uint32_t i = a.over_g(rid), g = rid - i * (uint32_t)a.G;
-        const bool on = r < rows && c * 8 < D;
-        const __nv_bfloat16* src = on ? a.q + (int64_t)(w.t0 + i) * a.q_ts + (int64_t)(w.h * a.G + g) * a.q_hs + c * 8 : a.q;
-        copy16(dst + (r >> 7) * S::QTILE + swizzled(r & 127, c, 128), src, on ? 16 : 0);
-        if (few)
-          for (int k = 32; k < 128; k += 32) copy16(dst + swizzled(r + k, c, 128), src, on ? 16 : 0);
-      }
-      copies_landed();
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sy.q_full);
-    }
   } else {
     // ---------------------------------------------------------------- MMA
     if (lane == 0) {
