@@ -104,19 +104,23 @@ struct Shape {
   static constexpr int DP = DP_;                       // head_dim padded to 64, 128 or 256
   static constexpr int NT = NT_;
   static constexpr int BN = DP == 256 ? 64 : 128;      // keys per tile
-  static constexpr int SL = DP == 256 ? 4 : DP == 128 ? (NT == 2 ? 4 : 5) : (NT == 2 ? 6 : 8);   // ring slots
-  // load warps per slot: converting e4m3 codes takes one warp longer than a
-  // slot's share of the memory bandwidth
-  static constexpr int LW = F8 && NT == 1 && DP > 64 ? 2 : 1;
-  // A tile of at most 32 rows, NT = 1 and 128 keys: see k_attend.
-  static constexpr bool FEW = NT == 1 && BN == 128;
   static constexpr int SLOT = BN * DP * 2;
   static constexpr int QTILE = 128 * DP * 2;
-  static constexpr int W_LOAD = NT * 4, N_LOAD = SL * LW, W_MMA = W_LOAD + N_LOAD;
+  static constexpr int SL = F8 ? (DP == 64 ? 6 : 4) : DP == 256 ? 4 : DP == 128 ? (NT == 2 ? 4 : 5) : (NT == 2 ? 6 : 8);   // ring slots
+  // Load warps. bf16: one per slot. e4m3: CW that convert each tile together, so
+  // that a slot is not held longer than its share of the time, and one that
+  // brings the codes AHEAD tiles before.
+  static constexpr int CW = F8 ? (NT == 1 ? 8 : 4) : 0;
+  static constexpr int N_LOAD = F8 ? CW : SL;
+  static constexpr int AHEAD = F8 ? (DP == 64 ? 4 : DP == 128 && NT == 1 ? 3 : 2) : 0;
+  static constexpr int RAW = BN * DP;                  // bytes of a tile's codes
+  // A tile of at most 32 rows, NT = 1 and 128 keys: see k_attend.
+  static constexpr bool FEW = NT == 1 && BN == 128;
+  static constexpr int W_LOAD = NT * 4, W_FETCH = W_LOAD + N_LOAD, W_MMA = W_FETCH + (F8 ? 1 : 0);
   static constexpr int THREADS = (W_MMA + 1) * 32;
   static constexpr int T_S = NT == 2 ? 128 : BN;       // TMEM columns between S buffers
   static constexpr int T_O = NT == 2 ? 256 : 2 * BN;   // first column of O
-  static constexpr size_t SMEM = 1024 + (size_t)NT * QTILE + (size_t)SL * SLOT + (FEW ? 4 * 32 * 64 + 4 * 32 * 8 : 0) + 512;
+  static constexpr size_t SMEM = 1024 + (size_t)NT * QTILE + (size_t)SL * SLOT + (size_t)AHEAD * RAW + (FEW ? 4 * 32 * 64 + 4 * 32 * 8 : 0) + 1024;
   static_assert(8 * (kMaxBatch + 1) <= SL * SLOT, "the plan's sums lie in the ring before it is used");
   static_assert(T_O + NT * DP <= TMEM_COLS, "TMEM");
   static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -284,7 +288,8 @@ struct Sync {
   uint64_t s_full[2], p_full[2];   // S ready; P stored
   uint64_t o_done[2], o_free[2];   // P V done; O read
   uint64_t q_full, q_free, fin;
-  uint64_t raw[10];                // e4m3: a load warp's codes have landed
+  uint64_t raw[4], taken[4];       // e4m3: a tile's codes have landed, and have been converted
+  uint8_t exps[4][128];            // their rows' exponents
   uint64_t merge;                  // between the four warps that share a tile's rows
   uint32_t tmem;
   int abort, nonfinite;
@@ -437,45 +442,38 @@ __device__ __forceinline__ void codes16_to_bf16(const uint4& v, uint32_t pow, fl
   }
 }
 
-// The cache rows of this warp's share of a key tile: rows lane, lane + 32, ...
-// of the BN / LW from position j0 on; -1 beyond the sequence or without a page.
+// The cache rows of a key tile: rows lane, lane + 32, ... from position j0 on; -1
+// beyond the sequence or without a page.
 template <class S, typename W>
 __device__ __forceinline__ void find_rows(const W& w, int64_t j0, int* row) {
   const int32_t* table = w.a.w.b.page_table + (int64_t)w.b * w.a.w.b.table_stride;
   const int64_t L = w.keys();
 #pragma unroll
-  for (int p = 0; p < S::BN / S::LW / 32; ++p) {
+  for (int p = 0; p < S::BN / 32; ++p) {
     const int64_t j = j0 + p * 32 + (threadIdx.x & 31);
     row[p] = j < L ? kv_row(w.a.w, table, j, w.h) : -1;
   }
 }
+// The same for TMA: the first row of the lane's copy (a.box rows of a 64-column
+// block); whether all rows of the tile are there.
+template <class S, typename W>
+__device__ __forceinline__ bool find_boxes(const W& w, int64_t j0, int* first) {
+  const int run = (threadIdx.x & 31) / (S::DP / 64) * w.a.box;
+  *first = 0;
+  if (w.a.box == 0 || j0 + S::BN > w.keys()) return false;
+  if (run < S::BN) *first = kv_row(w.a.w, w.a.w.b.page_table + (int64_t)w.b * w.a.w.b.table_stride, j0 + run, w.h);
+  return __all_sync(0xffffffffu, *first >= 0) != 0;
+}
 
-// Single rows. One warp copies its share of a ring slot (rows r0 to r0 + BN / LW;
-// zeros for a row of -1); e4m3 codes go where convert() takes them from.
-//
-// e4m3: the codes lie in the upper half of the warp's part of the slot and are
-// converted in place. In order of 64-column blocks and rows, 16 codes at offset
-// x of the codes become 32 bytes at offset 2x of the part, which holds only
-// codes already read; so the whole tile is in flight at once, without
-// registers or a staging buffer.
+// Single rows. One warp copies a key tile (zeros for a row of -1): bf16 to a ring
+// slot, e4m3 codes to their buffer, blocks of 64 columns with 64-byte rows.
 template <class S>
-struct Part {                                      // byte `lin` of the warp's part of a slot
-  static constexpr int RW = S::BN / S::LW, HALF = RW * 64, NB = S::DP / 64;
-  uint32_t slot;
-  int r0;
-  __device__ __forceinline__ uint32_t at(uint32_t lin) const {   // blocks of 2 HALF bytes, BN rows apart
-    return slot + lin / (2 * HALF) * (S::BN * 128) + r0 * 128 + lin % (2 * HALF);
-  }
-};
-
-template <class S>
-__device__ __forceinline__ void copy_rows(const Args& a, const void* pages, const int* row, int r0, uint32_t slot) {
-  constexpr int RW = S::BN / S::LW;
+__device__ __forceinline__ void copy_rows(const Args& a, const void* pages, const int* row, uint32_t dst) {
   const int lane = threadIdx.x & 31, D = a.w.c.head_dim;
   auto pick = [&](int p) {                         // row[p], by selects
     int x = row[0];
 #pragma unroll
-    for (int t = 1; t < RW / 32; ++t) x = p == t ? row[t] : x;
+    for (int t = 1; t < S::BN / 32; ++t) x = p == t ? row[t] : x;
     return x;
   };
   if constexpr (!S::F8) {
@@ -484,61 +482,49 @@ __device__ __forceinline__ void copy_rows(const Args& a, const void* pages, cons
     const bool in = c * 8 < D;
     const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(pages) + c * 8;
 #pragma unroll 1
-    for (int p = 0; p < RW / 32; ++p) {
+    for (int p = 0; p < S::BN / 32; ++p) {
       const int mine = pick(p);
 #pragma unroll 8
       for (int it = 0; it < 32 / RPI; ++it) {
         const int r = it * RPI + lane / CPR;
         const int cr = __shfl_sync(0xffffffffu, mine, r);
         const bool on = in && cr >= 0;
-        copy16(slot + swizzled(r0 + p * 32 + r, c, S::BN), on ? base + (int64_t)cr * D : a.q, on ? 16 : 0);
+        copy16(dst + swizzled(p * 32 + r, c, S::BN), on ? base + (int64_t)cr * D : a.q, on ? 16 : 0);
       }
     }
   } else {
-    using P = Part<S>;
-    const P part{slot, r0};
     const int q = lane & 3, rl = lane >> 2;        // 16-code chunk of a block's row; row of 8
     const uint8_t* base = static_cast<const uint8_t*>(pages) + q * 16;
 #pragma unroll 1
-    for (int n = 0; n < P::NB * (RW / 32); ++n) {
-      const int cb = n / (RW / 32), mine = pick(n % (RW / 32));
+    for (int n = 0; n < S::DP / 64 * (S::BN / 32); ++n) {
+      const int cb = n / (S::BN / 32), p = n % (S::BN / 32), mine = pick(p);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int cr = __shfl_sync(0xffffffffu, mine, k * 8 + rl);
         const bool on = cr >= 0 && cb * 64 + q * 16 < D;
-        copy16(part.at(P::NB * P::HALF + n * 2048) + k * 512 + lane * 16,
+        copy16(dst + (cb * S::BN + p * 32 + k * 8) * 64 + lane * 16,
                on ? base + (int64_t)cr * D + cb * 64 : (const void*)a.q, on ? 16 : 0);
       }
     }
   }
-  copies_landed();
-  __syncwarp();
 }
 
-// A run of rows at a time: the lanes' TMA copies of the warp's share, counted on
-// `bar`. Every row has a page, so that only the first of each run is looked up.
+// Runs of rows: the lanes' TMA copies of a key tile, counted on `bar`.
 template <class S>
-__device__ __forceinline__ void copy_boxes(const Args& a, const CUtensorMap* map, const int* row, int r0, uint32_t slot,
-                                           uint64_t* bar) {
-  using P = Part<S>;
+__device__ __forceinline__ void copy_boxes(const Args& a, const CUtensorMap* map, int first, uint32_t dst, uint64_t* bar) {
+  constexpr int NB = S::DP / 64;
   const int lane = threadIdx.x & 31;
-  const int run = lane / P::NB * a.box, cb = lane % P::NB;      // the lane's rows and 64-column block
-  int first = 0;
-#pragma unroll
-  for (int p = 0; p < P::RW / 32; ++p) {
-    const int t = __shfl_sync(0xffffffffu, row[p], run & 31);
-    if (run >> 5 == p) first = t;
-  }
-  fence_async_shared();                            // after the slot's earlier ordinary writes
-  if (lane == 0) mbar_expect_tx(bar, P::NB * P::HALF * (S::F8 ? 1 : 2));
+  const int run = lane / NB * a.box, cb = lane % NB;            // the lane's rows and 64-column block
+  fence_async_shared();                            // after the buffer's earlier ordinary accesses
+  if (lane == 0) mbar_expect_tx(bar, S::BN * S::DP * (S::F8 ? 1 : 2));
   __syncwarp();
-  if (run >= P::RW) return;
-  const uint32_t dst = S::F8 ? Part<S>{slot, r0}.at(P::NB * P::HALF + cb * P::HALF + run * 64)
-                             : slot + cb * (S::BN * 128) + run * 128;
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(cb * 64), "r"(first)
-      : "memory");
+  if (run < S::BN)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            dst + (cb * S::BN + run) * (S::F8 ? 64 : 128)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(cb * 64), "r"(first)
+        : "memory");
+  __syncwarp();
 }
 
 // Warp `part` of N_LOAD brings its share of the item's query rows.
@@ -562,70 +548,54 @@ __device__ __forceinline__ void load_queries(const W& w, int part, uint32_t dst)
   copies_landed();
 }
 
-// The exponents of the warp's rows (127 for a row of -1).
+// e4m3: rows r0 to r0 + BN / CW of a tile of codes to bf16 in a ring slot.
 template <class S>
-__device__ __forceinline__ void find_exps(const uint8_t* exps, const int* row, int* e) {
-#pragma unroll
-  for (int p = 0; p < S::BN / S::LW / 32; ++p)
-    e[p] = row[p] >= 0 ? max(1, min(254, (int)__ldg(exps + row[p]))) : 127;
-}
-
-// e4m3: the warp's codes to bf16, in place. `clean`: as in clean_rows.
-template <class S>
-__device__ __forceinline__ void convert(const int* exps, int r0, uint32_t slot, bool clean, Sync& sy) {
-  using P = Part<S>;
-  constexpr int G32 = P::RW / 32;                     // groups of 32 rows
-  const P part{slot, r0};
+__device__ __forceinline__ void convert(const uint8_t* exps, int r0, uint32_t src, uint32_t slot) {
+  constexpr int RW = S::BN / S::CW, K = RW / 8, NB = S::DP / 64;
   const int lane = threadIdx.x & 31, q = lane & 3, rl = lane >> 2;
-  bool large = false;
+  uint32_t e[K], large = 0;
 #pragma unroll
-  for (int p = 0; p < G32; ++p) large |= exps[p] > 134;
-  large = __any_sync(0xffffffffu, large);
-  // 64 columns of 32 rows at a time. The loop stays a loop: unrolled, its code
-  // streamed through the instruction cache and took four times as long.
+  for (int k = 0; k < K; ++k) {
+    // any byte is an exponent, also in rows never written
+    e[k] = max(1u, min(254u, (uint32_t)exps[r0 + k * 8 + rl]));
+    large |= e[k] > 134;
+  }
+  const bool conversions = __any_sync(0xffffffffu, large);
+  uint4 v[K];
+  auto load = [&](int cb) {
+    const uint32_t at = src + (cb * S::BN + r0) * 64 + lane * 16;
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = ld_shared(at + k * 512);
+  };
+  const uint32_t c0 = ((2 * q) ^ rl) << 4, c1 = ((2 * q + 1) ^ rl) << 4;
+  // The loop stays a loop: unrolled, its code streamed through the instruction
+  // cache and took four times as long.
+  load(0);
 #pragma unroll 1
-  for (int n = 0; n < P::NB * G32; ++n) {
-    const int cb = n / G32, p = n % G32;
-    int ee = exps[0];
+  for (int cb = 0; cb < NB; ++cb) {
+    const uint32_t to = slot + cb * (S::BN * 128) + (r0 + rl) * 128;
 #pragma unroll
-    for (int t = 1; t < G32; ++t) ee = p == t ? exps[t] : ee;
-    uint4 v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = ld_shared(part.at(P::NB * P::HALF + n * 2048) + k * 512 + lane * 16);
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = r0 + p * 32 + k * 8 + rl;
-      const uint32_t e = __shfl_sync(0xffffffffu, ee, k * 8 + rl);
+    for (int k = 0; k < K; ++k) {
       uint32_t o[8];
-      codes16_to_bf16(v[k], min(e + 120, 254u) * 0x00800080u, __uint_as_float(e << 23), large, o);
-      if (clean) {
-        bool dirty = false;
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          const uint32_t g = only_finite(o[t]);
-          dirty |= g != o[t];
-          o[t] = g;
-        }
-        if (dirty) *(volatile int*)&sy.nonfinite = 1;
-      }
-      st_shared(slot + swizzled(r, cb * 8 + 2 * q, S::BN), make_uint4(o[0], o[1], o[2], o[3]));
-      st_shared(slot + swizzled(r, cb * 8 + 2 * q + 1, S::BN), make_uint4(o[4], o[5], o[6], o[7]));
+      codes16_to_bf16(v[k], min(e[k] + 120, 254u) * 0x00800080u, __uint_as_float(e[k] << 23), conversions, o);
+      st_shared(to + k * 1024 + c0, make_uint4(o[0], o[1], o[2], o[3]));
+      st_shared(to + k * 1024 + c1, make_uint4(o[4], o[5], o[6], o[7]));
     }
-    __syncwarp();
+    if (cb + 1 < NB) load(cb + 1);
   }
 }
 
-// bf16: what is not finite in the warp's rows replaced by zero and noted. For
+// What is not finite in rows r0 to r0 + RW of a slot replaced by zero and noted. For
 // value tiles that hold positions which a query row of the item may not see:
 // 0 x NaN in the second product would reach every row.
-template <class S>
-__device__ __forceinline__ void clean_rows(uint32_t slot, Sync& sy) {
+template <class S, int RW>
+__device__ __forceinline__ void clean_rows(uint32_t slot, int r0, Sync& sy) {
   constexpr int CPR = S::DP / 8, RPI = 32 / CPR;
   const int lane = threadIdx.x & 31, c = lane % CPR;
   bool dirty = false;
-  for (int it = 0; it < S::BN / RPI; ++it) {
-    const uint32_t at = slot + swizzled(it * RPI + lane / CPR, c, S::BN);
+  __syncwarp();
+  for (int it = 0; it < RW / RPI; ++it) {
+    const uint32_t at = slot + swizzled(r0 + it * RPI + lane / CPR, c, S::BN);
     const uint4 v = ld_shared(at);
     const uint4 f = make_uint4(only_finite(v.x), only_finite(v.y), only_finite(v.z), only_finite(v.w));
     if (f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w) {
@@ -706,16 +676,17 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* ring = smem + S::NT * S::QTILE;
-  Sync& sy = *reinterpret_cast<Sync*>(ring + S::SL * S::SLOT);
-  static_assert(sizeof(Sync) <= 512 && S::SL <= 8 && (!S::F8 || S::SL * S::LW <= 10), "barriers");
-  float* few_o = reinterpret_cast<float*>(ring + S::SL * S::SLOT + 512);         // [4][32][16]
+  unsigned char* codes = ring + S::SL * S::SLOT;
+  Sync& sy = *reinterpret_cast<Sync*>(codes + S::AHEAD * S::RAW);
+  static_assert(sizeof(Sync) <= 1024 && S::SL <= 8 && S::N_LOAD <= 8 && S::AHEAD <= 4, "barriers");
+  float* few_o = reinterpret_cast<float*>(codes + S::AHEAD * S::RAW + 1024);         // [4][32][16]
   float2* few_ml = reinterpret_cast<float2*>(few_o + 4 * 32 * 16);              // [4][32]
   int64_t* pref = reinterpret_cast<int64_t*>(ring);
   constexpr int ROWS = S::NT * 128, BN = S::BN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S::SL; ++s) { mbar_init(&sy.full[s], S::LW); mbar_init(&sy.empty[s], 1); }
+    for (int s = 0; s < S::SL; ++s) { mbar_init(&sy.full[s], S::F8 ? S::CW : 1); mbar_init(&sy.empty[s], 1); }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sy.s_full[x], 1);
       mbar_init(&sy.p_full[x], 4);
@@ -726,7 +697,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     mbar_init(&sy.q_free, 1);
     mbar_init(&sy.fin, 1);
     mbar_init(&sy.merge, 4);
-    for (int x = 0; x < S::SL * S::LW && S::F8; ++x) mbar_init(&sy.raw[x], 1);
+    for (int x = 0; x < S::AHEAD; ++x) { mbar_init(&sy.raw[x], 33); mbar_init(&sy.taken[x], S::CW); }
     sy.abort = 0;
     sy.nonfinite = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1002,66 +973,117 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     }
   } else if (warp < S::W_MMA) {
     // ---------------------------------------------------------------- key and value loads
-    const int slot = (warp - S::W_LOAD) / S::LW, part = (warp - S::W_LOAD) % S::LW * (BN / S::LW);
-    const uint32_t dst = smem_u32(ring + slot * S::SLOT);
+    const int part = warp - S::W_LOAD;
+    const uint32_t ring0 = smem_u32(ring), codes0 = smem_u32(codes);
     bool ok = true;
-    uint32_t e = slot, uses = 0, raws = 0;            // this slot's next ring entry; its uses so far, by TMA
-    uint64_t* landing = nullptr;                      // where the last TMA copies arrive, and in which phase
-    uint32_t landed = 0;
-    uint32_t e0 = 0;                                  // the segment's first ring entry: tile tb's keys
-    uint32_t seg = 0;
-    for (; w.more() && ok; w.next(), ++seg) {
-      const uint32_t n = 2 * (uint32_t)(w.te - w.tb);
-      bool q_due = true;
-      for (;; e += S::SL) {
-        if (q_due && (e - e0 >= n || e >= e0 + S::SL)) {
-          q_due = false;
-          if (seg && !__all_sync(0xffffffffu, wait(&sy.q_free, (seg - 1) & 1, sy, a))) { ok = false; break; }
-          load_queries<S>(w, warp - S::W_LOAD, smem_u32(smem));
+    uint32_t e = 0, e0 = 0, seg = 0;                  // ring entry; the segment's first, tile tb's keys; segments
+    auto queries = [&]() {
+      if (seg && !__all_sync(0xffffffffu, wait(&sy.q_free, (seg - 1) & 1, sy, a))) return false;
+      load_queries<S>(w, part, smem_u32(smem));
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sy.q_full);
+      return true;
+    };
+    auto position = [&]() { return (int64_t)(w.tb + (int)((e - e0) >> 1)) * BN; };
+    auto to_clean = [&]() {                           // values that not every row of the item sees
+      return ((e - e0) & 1) && a.mask != DG_MASK_FULL && position() + BN > w.clear();
+    };
+    if constexpr (!S::F8) {
+      // one warp per slot, entries SL apart
+      bool landing = false;                           // the slot's last copy is by TMA, and has not been waited for
+      e = part;
+      for (; w.more() && ok; w.next(), ++seg) {
+        const uint32_t n = 2 * (uint32_t)(w.te - w.tb);
+        bool q_due = true;
+        for (;; e += S::SL) {
+          // the queries: after an entry whose slot waits for the segment before
+          if (q_due && (e - e0 >= n || e >= e0 + S::SL)) {
+            q_due = false;
+            if (!queries()) { ok = false; break; }
+          }
+          if (e - e0 >= n) break;
+          const bool kv = (e - e0) & 1, clean = to_clean();
+          const uint32_t dst = ring0 + part * S::SLOT;
+          int first, row[BN / 32];
+          const bool boxes = find_boxes<S>(w, position(), &first) && !clean;   // under the wait for the slot
+          if (!boxes) find_rows<S>(w, position(), row);
+          if (!__all_sync(0xffffffffu, wait(&sy.empty[part], ((e / S::SL) & 1) ^ 1, sy, a))) { ok = false; break; }
+          landing = boxes;
+          if (boxes) {                                // the copies arrive on `full` themselves
+            copy_boxes<S>(a, kv ? &v_map : &k_map, first, dst, &sy.full[part]);
+            continue;
+          }
+          copy_rows<S>(a, kv ? a.w.c.v : a.w.c.k, row, dst);
+          copies_landed();
+          if (clean) clean_rows<S, BN>(dst, 0, sy);
           fence_async_shared();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sy.q_full);
+          if (lane == 0) mbar_arrive(&sy.full[part]);
         }
-        if (e - e0 >= n) break;
-
-        const bool kv = (e - e0) & 1;
-        const int64_t j0 = (int64_t)(w.tb + (int)((e - e0) >> 1)) * BN;
-        int row[BN / S::LW / 32], exps[BN / S::LW / 32];
-        find_rows<S>(w, j0 + part, row);              // under the wait for the slot
-        if (S::F8) find_exps<S>(kv ? a.w.c.v_exp : a.w.c.k_exp, row, exps);
-        const bool clean = kv && a.mask != DG_MASK_FULL && j0 + BN > w.clear();
-        // by TMA unless a row is to be left out or looked through
-        bool boxes = a.box && !clean;
-#pragma unroll
-        for (int p = 0; p < BN / S::LW / 32; ++p) boxes = boxes && row[p] >= 0;
-        boxes = __all_sync(0xffffffffu, boxes);
-        if (!__all_sync(0xffffffffu, wait(&sy.empty[slot], (uses & 1) ^ 1, sy, a))) { ok = false; break; }
-        ++uses;
-        if (boxes) {
-          uint64_t* bar = S::F8 ? &sy.raw[warp - S::W_LOAD] : &sy.full[slot];
-          copy_boxes<S>(a, kv ? &v_map : &k_map, row, part, dst, bar);
-          landing = bar;
-          landed = (S::F8 ? raws : uses - 1) & 1;
-          if constexpr (S::F8) {
-            if (!__all_sync(0xffffffffu, wait(bar, raws & 1, sy, a))) { ok = false; break; }
-            ++raws;
-          } else {
-            continue;                                 // the copies arrive on `full` themselves
-          }
-        } else {
-          copy_rows<S>(a, kv ? a.w.c.v : a.w.c.k, row, part, dst);
-          landing = nullptr;
-        }
-        if constexpr (S::F8) convert<S>(exps, part, dst, clean, sy);
-        else if (clean) clean_rows<S>(dst, sy);
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sy.full[slot]);
+        e0 += n;
       }
-      e0 += n;
+      // a CTA that gives up still waits for its last copies
+      if (landing) wait(&sy.full[part], (e / S::SL - 1) & 1, sy, a, false);
+    } else if (warp == S::W_FETCH) {
+      // codes and exponents, AHEAD tiles before they are converted
+      for (; w.more() && ok; w.next()) {
+        const uint32_t n = 2 * (uint32_t)(w.te - w.tb);
+        for (; e - e0 < n; ++e) {
+          const uint32_t at = e % S::AHEAD, dst = codes0 + at * S::RAW;
+          const bool kv = (e - e0) & 1;
+          const uint8_t* exps = kv ? a.w.c.v_exp : a.w.c.k_exp;
+          int first, row[BN / 32], eight = -1;
+          const bool boxes = find_boxes<S>(w, position(), &first);      // under the wait for the buffer
+          if (!boxes) find_rows<S>(w, position(), row);
+          else if (lane < BN / 8)
+            eight = kv_row(a.w, a.w.b.page_table + (int64_t)w.b * a.w.b.table_stride, position() + lane * 8, w.h);
+          if (!__all_sync(0xffffffffu, wait(&sy.taken[at], ((e / S::AHEAD) & 1) ^ 1, sy, a))) { ok = false; break; }
+          if (boxes) {
+            copy_boxes<S>(a, kv ? &v_map : &k_map, first, dst, &sy.raw[at]);
+            if (eight >= 0)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(&sy.exps[at][lane * 8])), "l"(exps + eight)
+                           : "memory");
+          } else {
+            copy_rows<S>(a, kv ? a.w.c.v : a.w.c.k, row, dst);
+#pragma unroll
+            for (int p = 0; p < BN / 32; ++p)
+              sy.exps[at][p * 32 + lane] = row[p] >= 0 ? __ldg(exps + row[p]) : (uint8_t)127;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sy.raw[at]);
+          }
+          // one arrival of each lane when its own copies have landed
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sy.raw[at])) : "memory");
+        }
+        e0 += n;
+      }
+      // as above: of the last AHEAD tiles
+      for (uint32_t x = e > S::AHEAD ? e - S::AHEAD : 0; x < e; ++x)
+        wait(&sy.raw[x % S::AHEAD], (x / S::AHEAD) & 1, sy, a, false);
+    } else {
+      // all warps together on every entry, each its own rows
+      constexpr int RW = BN / S::CW;
+      const int r0 = part * RW;
+      for (; w.more() && ok; w.next(), ++seg) {
+        const uint32_t n = 2 * (uint32_t)(w.te - w.tb);
+        for (; e - e0 < n; ++e) {
+          const uint32_t at = e % S::AHEAD, slot = e % S::SL, dst = ring0 + slot * S::SLOT;
+          if (!__all_sync(0xffffffffu, wait(&sy.raw[at], (e / S::AHEAD) & 1, sy, a)) ||
+              !__all_sync(0xffffffffu, wait(&sy.empty[slot], ((e / S::SL) & 1) ^ 1, sy, a))) { ok = false; break; }
+          convert<S>(sy.exps[at], r0, codes0 + at * S::RAW, dst);
+          if (to_clean()) clean_rows<S, RW>(dst, r0, sy);
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sy.full[slot]);
+            mbar_arrive(&sy.taken[at]);
+          }
+          // the queries, once the first entry is on its way
+          if (e == e0 && !queries()) { ok = false; break; }
+        }
+        e0 += n;
+      }
     }
-    // a CTA that gives up still waits for its last copies
-    if (landing) wait(landing, landed, sy, a, false);
   } else {
     // ---------------------------------------------------------------- MMA
     if (lane == 0) {
@@ -1286,10 +1308,11 @@ Plan make_plan(const dg_kv_cache& c, const dg_kv_batch& b, int q_heads) {
 template <class S>
 cudaError_t launch(Args a, int ctas, cudaStream_t s) {
   // TMA copies take runs of rows that lie together: a power of two that divides
-  // page_size, at least 8 (one swizzle pattern) and at most a warp's share
+  // page_size, at least 8 (one swizzle pattern, and the exponents' 8 bytes)
   const dg_kv_cache& c = a.w.c;
-  a.box = std::min(c.page_size & -c.page_size, S::BN / S::LW);
+  a.box = std::min(c.page_size & -c.page_size, S::BN);
   if (a.box < 8 || c.head_dim < 64 || c.pages == 0) a.box = 0;
+  if (S::F8 && (reinterpret_cast<uintptr_t>(c.k_exp) | reinterpret_cast<uintptr_t>(c.v_exp)) % 8) a.box = 0;
   alignas(64) CUtensorMap maps[2] = {};
   const uint64_t rows = (uint64_t)c.pages * c.kv_heads * c.page_size;
   if (a.box && (!tc_encode_2d_rows(&maps[0], c.k, c.head_dim, rows, 64, a.box, S::F8) ||
