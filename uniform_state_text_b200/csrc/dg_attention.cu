@@ -454,15 +454,31 @@ __device__ __forceinline__ void find_rows(const W& w, int64_t j0, int* row) {
     row[p] = j < L ? kv_row(w.a.w, table, j, w.h) : -1;
   }
 }
-// The same for TMA: the first row of the lane's copy (a.box rows of a 64-column
-// block); whether all rows of the tile are there.
+// 32 entries of a sequence's page table in the lanes of a warp: a look-up per tile
+// had cost more than the tile's copies.
+struct Pages {
+  int b = -1, base = 0, page = 0;
+};
+// The same for TMA, by eights (a.box != 0: page_size is a multiple of 8): lane l
+// gets the cache row of position j0 + 8 l, l < BN / 8; whether all rows of the
+// tile are there.
 template <class S, typename W>
-__device__ __forceinline__ bool find_boxes(const W& w, int64_t j0, int* first) {
-  const int run = (threadIdx.x & 31) / (S::DP / 64) * w.a.box;
-  *first = 0;
+__device__ __forceinline__ bool find_eights(const W& w, Pages& pg, int64_t j0, int* eight) {
+  *eight = -1;
   if (w.a.box == 0 || j0 + S::BN > w.keys()) return false;
-  if (run < S::BN) *first = kv_row(w.a.w, w.a.w.b.page_table + (int64_t)w.b * w.a.w.b.table_stride, j0 + run, w.h);
-  return __all_sync(0xffffffffu, *first >= 0) != 0;
+  const dg_kv_cache& c = w.a.w.c;
+  const int lane = threadIdx.x & 31;
+  const uint32_t ps = (uint32_t)c.page_size, lo = (uint32_t)j0 / ps, j = (uint32_t)j0 + lane * 8, at = j / ps;
+  if (pg.b != w.b || (int)lo < pg.base || (int)(((uint32_t)j0 + S::BN - 8) / ps) >= pg.base + 32) {
+    pg.b = w.b;
+    pg.base = (int)lo;
+    const int64_t t = (int64_t)lo + lane;
+    pg.page = t < w.a.w.b.table_stride ? __ldg(w.a.w.b.page_table + (int64_t)w.b * w.a.w.b.table_stride + t) : -1;
+  }
+  const int page = __shfl_sync(0xffffffffu, pg.page, (int)at - pg.base);
+  if (lane < S::BN / 8 && page >= 0 && page < c.pages)
+    *eight = (page * c.kv_heads + w.h) * c.page_size + (int)(j - at * ps);
+  return __all_sync(0xffffffffu, *eight >= 0 || lane >= S::BN / 8) != 0;
 }
 
 // Single rows. One warp copies a key tile (zeros for a row of -1): bf16 to a ring
@@ -509,13 +525,14 @@ __device__ __forceinline__ void copy_rows(const Args& a, const void* pages, cons
   }
 }
 
-// Runs of rows: the lanes' TMA copies of a key tile, counted on `bar`.
+// Runs of rows: the lanes' TMA copies of a key tile, counted on `bar`. (Whoever
+// last used the buffer has fenced its ordinary accesses.)
 template <class S>
-__device__ __forceinline__ void copy_boxes(const Args& a, const CUtensorMap* map, int first, uint32_t dst, uint64_t* bar) {
+__device__ __forceinline__ void copy_boxes(const Args& a, const CUtensorMap* map, int eight, uint32_t dst, uint64_t* bar) {
   constexpr int NB = S::DP / 64;
   const int lane = threadIdx.x & 31;
   const int run = lane / NB * a.box, cb = lane % NB;            // the lane's rows and 64-column block
-  fence_async_shared();                            // after the buffer's earlier ordinary accesses
+  const int first = __shfl_sync(0xffffffffu, eight, (run >> 3) & 31);
   if (lane == 0) mbar_expect_tx(bar, S::BN * S::DP * (S::F8 ? 1 : 2));
   __syncwarp();
   if (run < S::BN)
@@ -976,6 +993,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     const int part = warp - S::W_LOAD;
     const uint32_t ring0 = smem_u32(ring), codes0 = smem_u32(codes);
     bool ok = true;
+    Pages pages;
     uint32_t e = 0, e0 = 0, seg = 0;                  // ring entry; the segment's first, tile tb's keys; segments
     auto queries = [&]() {
       if (seg && !__all_sync(0xffffffffu, wait(&sy.q_free, (seg - 1) & 1, sy, a))) return false;
@@ -1005,13 +1023,13 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           if (e - e0 >= n) break;
           const bool kv = (e - e0) & 1, clean = to_clean();
           const uint32_t dst = ring0 + part * S::SLOT;
-          int first, row[BN / 32];
-          const bool boxes = find_boxes<S>(w, position(), &first) && !clean;   // under the wait for the slot
+          int eight, row[BN / 32];
+          const bool boxes = find_eights<S>(w, pages, position(), &eight) && !clean;   // under the wait for the slot
           if (!boxes) find_rows<S>(w, position(), row);
           if (!__all_sync(0xffffffffu, wait(&sy.empty[part], ((e / S::SL) & 1) ^ 1, sy, a))) { ok = false; break; }
           landing = boxes;
           if (boxes) {                                // the copies arrive on `full` themselves
-            copy_boxes<S>(a, kv ? &v_map : &k_map, first, dst, &sy.full[part]);
+            copy_boxes<S>(a, kv ? &v_map : &k_map, eight, dst, &sy.full[part]);
             continue;
           }
           copy_rows<S>(a, kv ? a.w.c.v : a.w.c.k, row, dst);
@@ -1033,14 +1051,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           const uint32_t at = e % S::AHEAD, dst = codes0 + at * S::RAW;
           const bool kv = (e - e0) & 1;
           const uint8_t* exps = kv ? a.w.c.v_exp : a.w.c.k_exp;
-          int first, row[BN / 32], eight = -1;
-          const bool boxes = find_boxes<S>(w, position(), &first);      // under the wait for the buffer
+          int eight, row[BN / 32];
+          const bool boxes = find_eights<S>(w, pages, position(), &eight);    // under the wait for the buffer
           if (!boxes) find_rows<S>(w, position(), row);
-          else if (lane < BN / 8)
-            eight = kv_row(a.w, a.w.b.page_table + (int64_t)w.b * a.w.b.table_stride, position() + lane * 8, w.h);
           if (!__all_sync(0xffffffffu, wait(&sy.taken[at], ((e / S::AHEAD) & 1) ^ 1, sy, a))) { ok = false; break; }
           if (boxes) {
-            copy_boxes<S>(a, kv ? &v_map : &k_map, first, dst, &sy.raw[at]);
+            copy_boxes<S>(a, kv ? &v_map : &k_map, eight, dst, &sy.raw[at]);
             if (eight >= 0)
               asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(&sy.exps[at][lane * 8])), "l"(exps + eight)
                            : "memory");
