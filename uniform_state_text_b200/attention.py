@@ -19,34 +19,41 @@ from . import (DG_BF16, DG_F32, DG_KV_BF16, DG_KV_E4M3, DG_MASK_CAUSAL, DG_MASK_
 _DTYPES = {torch.bfloat16: DG_BF16, torch.float32: DG_F32}
 
 
-def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+def _call(index: int, fn, *args) -> None:
+    """fn(*args, stream) on torch's current stream of device `index`, that device current."""
+    stream = torch.cuda.current_stream(index).cuda_stream
+    if torch.cuda.current_device() == index:
+        fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            fn(*args, stream)
 
 
 def _dtype(t) -> int:
     try:
-        return _DTYPES[t if isinstance(t, torch.dtype) else t.dtype]
+        return _DTYPES[t]
     except KeyError:
         raise ValueError(f"dtype must be bfloat16 or float32, not {t}") from None
 
 
-def _rows(name, t, heads, head_dim, device, tokens=None):
+def _rows(name, t, heads, head_dim, index, tokens=None):
     """Check a [tokens, heads, head_dim] argument; returns its (token, head) strides."""
-    if t.dim() != 3 or t.device != device or (tokens is not None and t.shape[0] != tokens) \
-            or (heads is not None and t.shape[1] != heads) or t.shape[2] != head_dim:
+    shape = t.shape
+    if len(shape) != 3 or t.get_device() != index or (tokens is not None and shape[0] != tokens) \
+            or (heads is not None and shape[1] != heads) or shape[2] != head_dim:
         raise ValueError(f"{name} must be [{'tokens' if tokens is None else tokens}, "
-                         f"{'heads' if heads is None else heads}, {head_dim}] on {device}, got "
-                         f"{tuple(t.shape)} on {t.device}")
+                         f"{'heads' if heads is None else heads}, {head_dim}] on cuda:{index}, got "
+                         f"{tuple(shape)} on {t.device}")
     st, sh, sd = t.stride()
     if sd != 1 and head_dim > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
     # a stride over a dimension of one element is never taken
-    return (st if t.shape[0] > 1 else 0), (sh if t.shape[1] > 1 else 0)
+    return (st if shape[0] > 1 else 0), (sh if shape[1] > 1 else 0)
 
 
-def _vector(name, t, dtype, device, n):
-    if t.dtype != dtype or t.device != device or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} on {device}")
+def _vector(name, t, dtype, index, n):
+    if t.dtype is not dtype or t.get_device() != index or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} on cuda:{index}")
     return t.data_ptr()
 
 
@@ -63,24 +70,25 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, *, interleaved: 
 
     weights: [D] of q's dtype, or None for ones; positions int32 [tokens]; inv_freq float64.
     """
-    dt, dev = _dtype(q), q.device
+    dt = q.dtype
+    code = _dtype(dt)
     if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
-    if k.dtype != q.dtype:
+    if k.dtype is not dt:
         raise ValueError("q and k must have one dtype")
-    tokens, hq, d = q.shape if q.dim() == 3 else (0, 0, 0)
-    qs = _rows("q", q, None, d, dev)
-    ks = _rows("k", k, None, d, dev, tokens)
-    hk, rot = k.shape[1], 2 * inv_freq.shape[0]
-    wq = _vector("q_weight", q_weight, q.dtype, dev, d) if q_weight is not None else 0
-    wk = _vector("k_weight", k_weight, q.dtype, dev, d) if k_weight is not None else 0
-    pos = _vector("positions", positions, torch.int32, dev, tokens)
-    freq = _vector("inv_freq", inv_freq, torch.float64, dev, rot // 2)
-    with torch.cuda.device(dev):
-        qo, ko = q.new_empty((tokens, hq, d)), k.new_empty((tokens, hk, d))
-        dg_qk_norm_rope(tokens, hq, hk, d, rot, interleaved, dt, q.data_ptr(), *qs, k.data_ptr(), *ks,
-                        wq, wk, weight_offset, eps, pos, freq, qo.data_ptr(), ko.data_ptr(),
-                        _stream(dev))
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [tokens, heads, head_dim]")
+    index = q.get_device()
+    tokens, hq, d = q.shape
+    hk, half = k.shape[1], inv_freq.shape[0]
+    qs, ks = _rows("q", q, None, d, index), _rows("k", k, None, d, index, tokens)
+    wq = _vector("q_weight", q_weight, dt, index, d) if q_weight is not None else None
+    wk = _vector("k_weight", k_weight, dt, index, d) if k_weight is not None else None
+    pos = _vector("positions", positions, torch.int32, index, tokens)
+    freq = _vector("inv_freq", inv_freq, torch.float64, index, half)
+    qo, ko = q.new_empty((tokens, hq, d)), k.new_empty((tokens, hk, d))
+    _call(index, dg_qk_norm_rope, tokens, hq, hk, d, 2 * half, interleaved, code, q.data_ptr(), *qs,
+          k.data_ptr(), *ks, wq, wk, weight_offset, eps, pos, freq, qo.data_ptr(), ko.data_ptr())
     return qo, ko
 
 
@@ -95,10 +103,11 @@ class KVBatch:
         if not page_table.is_cuda or page_table.dtype != torch.int32 or page_table.dim() != 2 \
                 or not page_table.is_contiguous():
             raise ValueError("page_table must be a contiguous int32 CUDA tensor [batch, pages]")
-        n = page_table.shape[0]
-        _vector("first", first, torch.int32, dev, n + 1)
-        _vector("past", past, torch.int32, dev, n)
-        self.page_table, self.first, self.past, self.tokens, self.device = page_table, first, past, int(tokens), dev
+        n, index = page_table.shape[0], page_table.get_device()
+        _vector("first", first, torch.int32, index, n + 1)
+        _vector("past", past, torch.int32, index, n)
+        self.page_table, self.first, self.past, self.tokens = page_table, first, past, int(tokens)
+        self.device, self.index = dev, index
         self.c = dg_kv_batch(page_table=page_table.data_ptr(), first=first.data_ptr(),
                              past=past.data_ptr(), batch=n, table_stride=page_table.shape[1],
                              tokens=self.tokens)
@@ -119,7 +128,8 @@ class KVCache:
                     or t.shape != shape or t.dtype != dt or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {dt} CUDA tensor {tuple(shape)}, pages "
                                  "[pages, kv_heads, page_size, head_dim] on one device")
-        self.k, self.v, self.k_exp, self.v_exp, self.device = k, v, k_exp, v_exp, dev
+        self.k, self.v, self.k_exp, self.v_exp, self.device, self.index = k, v, k_exp, v_exp, dev, k.get_device()
+        self._scratch = {}                  # bytes by (tokens, batch, q_heads)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         f8 = k.dtype != torch.bfloat16
         self.c = dg_kv_cache(k=k.data_ptr(), v=v.data_ptr(), k_exp=k_exp.data_ptr() if f8 else None,
@@ -144,36 +154,36 @@ class KVCache:
             raise DgError(code, "a cache call met a page or position outside the cache, or a wait ran out")
 
     def _batch(self, batch):
-        if batch.device != self.device:
+        if batch.index != self.index:
             raise ValueError(f"the batch is on {batch.device}, the cache on {self.device}")
 
     def write(self, k, v, batch: KVBatch) -> None:
         """Write k, v [tokens, kv_heads, head_dim] (bf16 or fp32) at the batch's positions."""
         self._batch(batch)
-        c = self.c
-        dt = _dtype(k)
-        if v.dtype != k.dtype:
+        c, index, tokens = self.c, self.index, batch.tokens
+        code = _dtype(k.dtype)
+        if v.dtype is not k.dtype:
             raise ValueError("k and v must have one dtype")
-        ks = _rows("k", k, c.kv_heads, c.head_dim, self.device, batch.tokens)
-        vs = _rows("v", v, c.kv_heads, c.head_dim, self.device, batch.tokens)
-        with torch.cuda.device(self.device):
-            dg_cache_write(c, batch.c, dt, k.data_ptr(), *ks, v.data_ptr(), *vs, _stream(self.device))
+        h, d = c.kv_heads, c.head_dim
+        ks, vs = _rows("k", k, h, d, index, tokens), _rows("v", v, h, d, index, tokens)
+        _call(index, dg_cache_write, c, batch.c, code, k.data_ptr(), *ks, v.data_ptr(), *vs)
 
     def read(self, batch: KVBatch, dtype=torch.bfloat16, out=None):
         """The batch's rows as (k, v) [tokens, kv_heads, head_dim]; padding rows are not written."""
         self._batch(batch)
-        c = self.c
-        dt = _dtype(dtype)
-        with torch.cuda.device(self.device):
-            if out is None:
-                shape = (batch.tokens, c.kv_heads, c.head_dim)
-                out = tuple(torch.empty(shape, dtype=dtype, device=self.device) for _ in "kv")
-            for t in out:
-                _rows("out", t, c.kv_heads, c.head_dim, self.device, batch.tokens)
-                if t.dtype != dtype or not t.is_contiguous():
+        c, index = self.c, self.index
+        code = _dtype(dtype)
+        if out is None:
+            shape = (batch.tokens, c.kv_heads, c.head_dim)
+            k, v = (torch.empty(shape, dtype=dtype, device=self.device) for _ in "kv")
+        else:
+            k, v = out
+            for t in (k, v):
+                _rows("out", t, c.kv_heads, c.head_dim, index, batch.tokens)
+                if t.dtype is not dtype or not t.is_contiguous():
                     raise ValueError(f"out must be contiguous {dtype}")
-            dg_cache_read(c, batch.c, dt, out[0].data_ptr(), out[1].data_ptr(), _stream(self.device))
-        return out
+        _call(index, dg_cache_read, c, batch.c, code, k.data_ptr(), v.data_ptr())
+        return k, v
 
     def attend(self, q, batch: KVBatch, mask: int, *, tree=None, scale: float | None = None, out=None,
                lse=None):
@@ -185,30 +195,34 @@ class KVCache:
         given; padding rows are not written.
         """
         self._batch(batch)
-        c, dev = self.c, self.device
-        if q.dtype != torch.bfloat16:
+        c, index, tokens = self.c, self.index, batch.tokens
+        if q.dtype is not torch.bfloat16:
             raise ValueError("q must be bfloat16")
-        qs = _rows("q", q, None, c.head_dim, dev, batch.tokens)
-        hq, words, tree_ptr = q.shape[1], 0, 0
+        qs = _rows("q", q, None, c.head_dim, index, tokens)
+        hq, words, tree_ptr = q.shape[1], 0, None
         if mask == DG_MASK_TREE:
-            if tree is None or tree.dtype != torch.int32 or tree.device != dev or tree.dim() != 2 \
-                    or tree.shape[0] != batch.tokens or not tree.is_contiguous():
-                raise ValueError(f"tree must be a contiguous int32 tensor [{batch.tokens}, words] on {dev}")
+            if tree is None or tree.dtype is not torch.int32 or tree.get_device() != index or tree.dim() != 2 \
+                    or tree.shape[0] != tokens or not tree.is_contiguous():
+                raise ValueError(f"tree must be a contiguous int32 tensor [{tokens}, words] on {self.device}")
             words, tree_ptr = tree.shape[1], tree.data_ptr()
         elif tree is not None:
             raise ValueError("tree goes with DG_MASK_TREE")
-        with torch.cuda.device(dev):
-            if out is None:
-                out = torch.empty((batch.tokens, hq, c.head_dim), dtype=torch.bfloat16, device=dev)
-            if lse is None:
-                lse = torch.empty((batch.tokens, hq), dtype=torch.float32, device=dev)
-            if out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous() \
-                    or lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous() \
-                    or out.device != dev or lse.device != dev:
-                raise ValueError("out must be contiguous bfloat16 of q's shape, lse float32 [tokens, q_heads]")
-            n = dg_cache_attention_scratch_bytes(c, batch.c, hq)
-            scratch = torch.empty(n, dtype=torch.uint8, device=dev)
-            dg_cache_attention(c, batch.c, hq, q.data_ptr(), *qs,
-                               c.head_dim ** -0.5 if scale is None else scale, mask, tree_ptr, words,
-                               out.data_ptr(), lse.data_ptr(), scratch.data_ptr(), n, _stream(dev))
+        if out is None:
+            out = torch.empty((tokens, hq, c.head_dim), dtype=torch.bfloat16, device=self.device)
+        elif out.dtype is not torch.bfloat16 or out.shape != q.shape or not out.is_contiguous() \
+                or out.get_device() != index:
+            raise ValueError("out must be contiguous bfloat16 of q's shape")
+        if lse is None:
+            lse = torch.empty((tokens, hq), dtype=torch.float32, device=self.device)
+        elif lse.dtype is not torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous() \
+                or lse.get_device() != index:
+            raise ValueError("lse must be contiguous float32 [tokens, q_heads]")
+        key = (tokens, batch.c.batch, hq)
+        n = self._scratch.get(key)
+        if n is None:
+            n = self._scratch[key] = dg_cache_attention_scratch_bytes(c, batch.c, hq)
+        scratch = torch.empty(n, dtype=torch.uint8, device=self.device)
+        _call(index, dg_cache_attention, c, batch.c, hq, q.data_ptr(), *qs,
+              c.head_dim ** -0.5 if scale is None else scale, mask, tree_ptr, words, out.data_ptr(),
+              lse.data_ptr(), scratch.data_ptr(), n)
         return out, lse

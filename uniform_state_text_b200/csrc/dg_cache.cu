@@ -24,7 +24,27 @@ namespace rows {
 
 constexpr int THREADS = 256;
 
-// 8 elements as fp32.
+// 4 and 8 elements as fp32.
+template <typename T> __device__ __forceinline__ void load4(const T* p, float* v);
+template <> __device__ __forceinline__ void load4<float>(const float* p, float* v) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+}
+template <> __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, float* v) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  v[0] = __uint_as_float(u.x << 16);
+  v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+  v[2] = __uint_as_float(u.y << 16);
+  v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+}
+template <typename T> __device__ __forceinline__ void store4(T* p, const float* v);
+template <> __device__ __forceinline__ void store4<float>(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* p, const float* v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
 template <typename T> __device__ __forceinline__ void load8(const T* p, float* v);
 template <> __device__ __forceinline__ void load8<float>(const float* p, float* v) {
   const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
@@ -64,7 +84,8 @@ struct NormArgs {
   int64_t q_ts, q_hs, k_ts, k_hs;
   const int32_t* pos;
   const double* freq;
-  int tokens, qh, kh, D, rot, chunk, nchunk;   // chunk: heads per group, nchunk: groups per token
+  int tokens, qh, kh, D, rot;
+  int tpb, hpb;                // tokens and heads per block
   float off, eps;
 };
 
@@ -85,76 +106,104 @@ __device__ __forceinline__ void sincos_turns(uint64_t phase, float* s, float* c)
   sincospif((float)(int32_t)(uint32_t)(phase >> 32) * 4.656612873077392578125e-10f, s, c);
 }
 
-// One group of LPR lanes takes `chunk` heads of one token: its lanes' cosines
-// and sines are computed once and serve all of them.
+// A block takes `hpb` heads of `tpb` tokens. Their cosines and sines, which cost
+// as much as the rest of several heads, are worked out once into shared memory,
+// and so are the weights in fp32; then a group of LPR lanes takes a row at a
+// time, two rows in flight. A lane has 4 pairs of the rotation, (4 l, 4 l + half)
+// or 8 neighbours, or else 8 elements behind rot, so that no element changes
+// lanes.
 template <typename T, int LPR, bool INTERLEAVED>
 __global__ void __launch_bounds__(THREADS) k_norm_rope(const NormArgs a) {
-  const int64_t unit = ((int64_t)blockIdx.x * THREADS + threadIdx.x) / LPR;
-  const int token = (int)(unit / a.nchunk);
-  const int sub = threadIdx.x % LPR;
-  const bool live = token < a.tokens;               // whole groups; dead ones still shuffle
-  const int h0 = (int)(unit % a.nchunk) * a.chunk;
-  const int nh = live ? min(a.chunk, a.qh + a.kh - h0) : 0;
-  const int x0 = sub * 8;
-  const bool in = x0 < a.D;
-  const bool turn = x0 < a.rot;
+  extern __shared__ float sh[];
+  constexpr int GROUPS = THREADS / LPR, ROWS = 2;
   const int half = a.rot / 2;
-  // this lane's rotations: 8 pairs with the other half's lane, or 4 of its own
-  float cs[INTERLEAVED ? 4 : 8], sn[INTERLEAVED ? 4 : 8];
-  if (turn && live) {
-    const int64_t pos = __ldg(a.pos + token);
-    const int p0 = INTERLEAVED ? x0 / 2 : (x0 < half ? x0 : x0 - half);
+  const int t0 = blockIdx.x * a.tpb, nt = min(a.tpb, a.tokens - t0);
+  const int h0 = blockIdx.y * a.hpb, nh = min(a.hpb, a.qh + a.kh - h0);
+  float* wq = sh;                                   // [D]
+  float* wk = wq + a.D;                             // [D]
+  float* cs = wk + a.D;                             // [tpb][half]
+  float* sn = cs + a.tpb * half;
+  const int g = threadIdx.x / LPR, sub = threadIdx.x % LPR, nr = nt * nh;
+  const bool turn = sub * 8 < a.rot, in = sub * 8 < a.D;
+  const int x0 = !INTERLEAVED && turn ? sub * 4 : sub * 8;          // elements x0 .. + 3
+  const int x1 = !INTERLEAVED && turn ? half + sub * 4 : x0 + 4;    // and x1 .. + 3
+  const uint32_t mul = nh > 1 ? 0xffffffffu / (uint32_t)nh + 1 : 0; // r / nh by the high half, exact for r < 2^16
+  float v[ROWS][8];
+  int64_t to[ROWS];                                 // the row's first element in its output; -1: none
+  bool is_q[ROWS];
+  int tok[ROWS];
+  auto load = [&](int r0) {
 #pragma unroll
-    for (int j = 0; j < (INTERLEAVED ? 4 : 8); ++j)
-      sincos_turns((uint64_t)pos * turns_per_position(__ldg(a.freq + p0 + j)), &sn[j], &cs[j]);
-  }
-  const int warp_lane = threadIdx.x & 31;
-  const int base = warp_lane - sub;                 // the group's first lane
-  const int mate = turn ? base + (x0 < half ? sub + half / 8 : sub - half / 8) : warp_lane;
-  // all groups of a warp run the same number of rounds, so that every lane shuffles
-  const int rounds = __reduce_max_sync(0xffffffffu, nh);
-  for (int r = 0; r < rounds; ++r) {
-    const bool on = r < nh && in;
-    const int h = h0 + r;
-    const bool is_q = h < a.qh;
-    const int hh = is_q ? h : h - a.qh;
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, w[8];
-    if (on) {
-      const T* src = is_q ? static_cast<const T*>(a.q) + token * a.q_ts + hh * a.q_hs
-                          : static_cast<const T*>(a.k) + token * a.k_ts + hh * a.k_hs;
-      load8(src + x0, v);
+    for (int i = 0; i < ROWS; ++i) {
+      const int r = r0 + i * GROUPS + g;
+      to[i] = -1;
+      is_q[i] = false;
+      tok[i] = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+      if (r >= nr) continue;
+      tok[i] = nh > 1 ? (int)__umulhi((uint32_t)r, mul) : r;
+      const int h = h0 + r - tok[i] * nh, t = t0 + tok[i];
+      is_q[i] = h < a.qh;
+      const T* src = is_q[i] ? static_cast<const T*>(a.q) + t * a.q_ts + h * a.q_hs
+                             : static_cast<const T*>(a.k) + t * a.k_ts + (h - a.qh) * a.k_hs;
+      to[i] = (is_q[i] ? (int64_t)t * a.qh + h : (int64_t)t * a.kh + h - a.qh) * a.D;
+      if (in) {
+        load4(src + x0, v[i]);
+        load4(src + x1, v[i] + 4);
+      }
     }
-    float ss = 0.f;
+  };
+  load(0);
+  for (int x = threadIdx.x; x < 2 * a.D; x += THREADS) {
+    const T* w = static_cast<const T*>(x < a.D ? a.wq : a.wk);
+    sh[x] = (w ? to_f32(w[x < a.D ? x : x - a.D]) : 1.0f) + a.off;
+  }
+  for (int x = threadIdx.x; x < nt * half; x += THREADS) {
+    const int t = x / half, p = x - t * half;
+    sincos_turns((uint64_t)(int64_t)__ldg(a.pos + t0 + t) * turns_per_position(__ldg(a.freq + p)), &sn[x], &cs[x]);
+  }
+  __syncthreads();
+  const float per = 1.0f / (float)a.D;
+  for (int r0 = 0; r0 < nr;) {                      // every lane of the block runs every round
+    float ss[ROWS];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+    for (int i = 0; i < ROWS; ++i) {
+      ss[i] = 0.f;
 #pragma unroll
-    for (int m = LPR / 2; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-    const float rs = 1.0f / sqrtf(ss / (float)a.D + a.eps);
-    const T* wp = static_cast<const T*>(is_q ? a.wq : a.wk);
-    if (on && wp) load8(wp + x0, w);
+      for (int j = 0; j < 8; ++j) ss[i] = fmaf(v[i][j], v[i][j], ss[i]);
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = v[j] * rs * ((wp && on ? w[j] : 1.0f) + a.off);
-    if constexpr (INTERLEAVED) {
+    for (int m = LPR / 2; m; m >>= 1)
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], m);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      if (to[i] < 0 || !in) continue;
+      const float rs = rsqrtf(fmaf(ss[i], per, a.eps));             // 2 ulp
+      const float* w = is_q[i] ? wq : wk;
+      const float4 w0 = *reinterpret_cast<const float4*>(w + x0), w1 = *reinterpret_cast<const float4*>(w + x1);
+      float y[8] = {v[i][0] * rs * w0.x, v[i][1] * rs * w0.y, v[i][2] * rs * w0.z, v[i][3] * rs * w0.w,
+                    v[i][4] * rs * w1.x, v[i][5] * rs * w1.y, v[i][6] * rs * w1.z, v[i][7] * rs * w1.w};
       if (turn) {
+        const float4 c = *reinterpret_cast<const float4*>(cs + tok[i] * half + sub * 4);
+        const float4 s = *reinterpret_cast<const float4*>(sn + tok[i] * half + sub * 4);
+        const float cc[4] = {c.x, c.y, c.z, c.w}, sc[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float x = v[2 * j], y = v[2 * j + 1];
-          v[2 * j] = x * cs[j] - y * sn[j];
-          v[2 * j + 1] = y * cs[j] + x * sn[j];
+          float& ya = y[INTERLEAVED ? 2 * j : j];
+          float& yb = y[INTERLEAVED ? 2 * j + 1 : j + 4];
+          const float p = ya * cc[j] - yb * sc[j];
+          yb = yb * cc[j] + ya * sc[j];
+          ya = p;
         }
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float o = __shfl_sync(0xffffffffu, v[j], mate);
-        if (turn) v[j] = x0 < half ? v[j] * cs[j] - o * sn[j] : v[j] * cs[j] + o * sn[j];
-      }
+      T* dst = static_cast<T*>(is_q[i] ? a.qo : a.ko) + to[i];
+      store4(dst + x0, y);
+      store4(dst + x1, y + 4);
     }
-    if (on) {
-      T* dst = is_q ? static_cast<T*>(a.qo) + ((int64_t)token * a.qh + hh) * a.D
-                    : static_cast<T*>(a.ko) + ((int64_t)token * a.kh + hh) * a.D;
-      store8(dst + x0, v);
-    }
+    r0 += ROWS * GROUPS;
+    load(r0);
   }
 }
 
@@ -182,11 +231,16 @@ __device__ __forceinline__ void write_row(const T* src, void* pages, uint8_t* ex
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (on) load8(src + x0, v);
   if constexpr (F8) {
-    float amax = 0.f;
+    float amax = 0.f;                                // (fmaxf passes over NaN)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float m = fabsf(v[j]);
-      amax = fmaxf(amax, m < INFINITY ? m : 0.f);     // NaN and infinities do not scale the row
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+    if (amax == INFINITY) {                          // infinities do not scale the row, and become NaN
+      amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (fabsf(v[j]) == INFINITY) v[j] = NAN;
+        else amax = fmaxf(amax, fabsf(v[j]));
+      }
     }
 #pragma unroll
     for (int m = LPR / 2; m; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
@@ -194,12 +248,8 @@ __device__ __forceinline__ void write_row(const T* src, void* pages, uint8_t* ex
     const float s = pow2(-e);
     uint32_t c[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float f[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = fabsf(v[4 * j + i]) < INFINITY ? v[4 * j + i] * s : NAN;
-      c[j] = f32x2_to_e4m3(f[0], f[1]) | ((uint32_t)f32x2_to_e4m3(f[2], f[3]) << 16);
-    }
+    for (int j = 0; j < 2; ++j)
+      c[j] = f32x2_to_e4m3(v[4 * j] * s, v[4 * j + 1] * s) | ((uint32_t)f32x2_to_e4m3(v[4 * j + 2] * s, v[4 * j + 3] * s) << 16);
     if (on) {
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pages) + (int64_t)row * D + x0) = make_uint2(c[0], c[1]);
       if (x0 == 0) exps[row] = (uint8_t)(e + 127);
@@ -244,8 +294,12 @@ __device__ __forceinline__ void read_row(const void* pages, const uint8_t* exps,
       // any byte is a power of two that fp32 holds, also in rows never written
       const float s = pow2(max(-126, min(127, (int)exps[row] - 127)));
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[j] = e4m3_to_f32((uint8_t)((j < 4 ? c.x : c.y) >> (8 * (j & 3)))) * s;
+      for (int j = 0; j < 4; ++j) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((j < 2 ? c.x : c.y) >> (16 * (j & 1))), __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        v[2 * j] = f.x * s;
+        v[2 * j + 1] = f.y * s;
+      }
     } else {
       load8(static_cast<const __nv_bfloat16*>(pages) + (int64_t)row * D + x0, v);
     }
@@ -253,20 +307,38 @@ __device__ __forceinline__ void read_row(const void* pages, const uint8_t* exps,
   store8(dst + x0, v);
 }
 
-template <typename T, int LPR, bool F8>
+// A group of LPR lanes per head and TOK neighbouring tokens, whose rows lie
+// together in their page: one search for the sequence, and 2 TOK rows in flight.
+template <typename T, int LPR, bool F8, int TOK>
 __global__ void __launch_bounds__(THREADS) k_cache_read(const __grid_constant__ ReadArgs a) {
   const KvView& w = a.w;
   const int64_t unit = ((int64_t)blockIdx.x * THREADS + threadIdx.x) / LPR;
-  const int token = (int)(unit / w.c.kv_heads), head = (int)(unit % w.c.kv_heads);
-  const int x0 = (threadIdx.x % LPR) * 8;
-  if (unit >= (int64_t)w.b.tokens * w.c.kv_heads || x0 >= w.c.head_dim) return;
-  const int b = kv_sequence(w, token);
-  if (b < 0) return;
-  const int row = kv_row(w, w.b.page_table + (int64_t)b * w.b.table_stride,
-                         (int64_t)__ldg(w.b.past + b) + (token - __ldg(w.b.first + b)), head);
-  const int64_t o = unit * w.c.head_dim;
-  read_row<T, F8>(w.c.k, w.c.k_exp, row, w.c.head_dim, x0, static_cast<T*>(a.k) + o);
-  read_row<T, F8>(w.c.v, w.c.v_exp, row, w.c.head_dim, x0, static_cast<T*>(a.v) + o);
+  const int head = (int)(unit % w.c.kv_heads), x0 = (threadIdx.x % LPR) * 8;
+  const int64_t t0 = unit / w.c.kv_heads * TOK;
+  if (t0 >= w.b.tokens || x0 >= w.c.head_dim) return;
+  int b = -1, row[TOK], end = 0;
+  int64_t shift = 0;                               // position less token
+#pragma unroll
+  for (int i = 0; i < TOK; ++i) {
+    const int token = (int)t0 + i;
+    row[i] = -2;
+    if (t0 + i >= w.b.tokens) continue;
+    if (i == 0 || token >= end) {
+      b = kv_sequence(w, token);
+      if (b >= 0) {
+        end = __ldg(w.b.first + b + 1);
+        shift = (int64_t)__ldg(w.b.past + b) - __ldg(w.b.first + b);
+      }
+    }
+    if (b >= 0) row[i] = kv_row(w, w.b.page_table + (int64_t)b * w.b.table_stride, token + shift, head);
+  }
+#pragma unroll
+  for (int i = 0; i < TOK; ++i) {
+    if (row[i] == -2) continue;                    // padding
+    const int64_t o = ((t0 + i) * w.c.kv_heads + head) * w.c.head_dim;
+    read_row<T, F8>(w.c.k, w.c.k_exp, row[i], w.c.head_dim, x0, static_cast<T*>(a.k) + o);
+    read_row<T, F8>(w.c.v, w.c.v_exp, row[i], w.c.head_dim, x0, static_cast<T*>(a.v) + o);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -362,20 +434,22 @@ extern "C" int dg_qk_norm_rope(int32_t tokens, int32_t q_heads, int32_t k_heads,
   if (off16(q_weight) || off16(k_weight)) return fail(DG_EINVAL, "weights must be 16-byte aligned");
   if (rot_dim && (!positions || !inv_freq)) return fail(DG_EINVAL, "a rotation needs positions and inv_freq");
   NormArgs a{q, k, q_weight, k_weight, q_out, k_out, q_ts, q_hs, k_ts, k_hs, positions, inv_freq,
-             tokens, q_heads, k_heads, head_dim, rot_dim, 1, (int)heads, weight_offset, eps};
+             tokens, q_heads, k_heads, head_dim, rot_dim, 1, 1, weight_offset, eps};
   const cudaError_t e = by_lanes(head_dim, [&](auto lpr) {
     constexpr int L = decltype(lpr)::value;
-    // As many heads per group as leave two full waves of threads, at most 8:
-    // they share the lane's sines and cosines.
-    const int64_t lanes = (int64_t)tokens * heads * L;
-    a.chunk = (int)std::min<int64_t>(std::min<int64_t>(8, heads), std::max<int64_t>(1, lanes / (148 * 2 * 2048)));
-    a.nchunk = (int)((heads + a.chunk - 1) / a.chunk);
-    const unsigned grid = blocks((int64_t)tokens * a.nchunk, L);
-    if (!grid) return cudaErrorInvalidConfiguration;
+    // A block has about four rounds of rows, so that the sines are shared by many
+    // rows; with few tokens, as few rows as one round takes, to fill the SMs.
+    const int64_t round = 2 * (THREADS / L), rows = (int64_t)tokens * heads;
+    const int64_t want = rows >= 148 * 4 * round ? 4 * round : round;
+    a.hpb = (int)std::min<int64_t>(heads, want);
+    a.tpb = (int)std::min<int64_t>(std::max<int64_t>(1, want / heads), tokens);
+    a.tpb = std::min(a.tpb, 32);
+    const dim3 grid((unsigned)((tokens + a.tpb - 1) / a.tpb), (unsigned)((heads + a.hpb - 1) / a.hpb));
+    const size_t smem = sizeof(float) * (2 * head_dim + a.tpb * rot_dim);   // at most 34 KB
     return by_type(dtype, [&](auto t) {
       using T = decltype(t);
-      if (interleaved) k_norm_rope<T, L, true><<<grid, THREADS, 0, (cudaStream_t)stream>>>(a);
-      else k_norm_rope<T, L, false><<<grid, THREADS, 0, (cudaStream_t)stream>>>(a);
+      if (interleaved) k_norm_rope<T, L, true><<<grid, THREADS, smem, (cudaStream_t)stream>>>(a);
+      else k_norm_rope<T, L, false><<<grid, THREADS, smem, (cudaStream_t)stream>>>(a);
       return cudaGetLastError();
     });
   });
@@ -420,10 +494,19 @@ extern "C" int dg_cache_read(const dg_kv_cache* cache, const dg_kv_batch* batch,
     constexpr int L = decltype(lpr)::value;
     const unsigned grid = blocks(n, L);
     if (!grid) return cudaErrorInvalidConfiguration;
+    // four tokens to a group once that still fills every SM
+    const bool many = n * L >= 4 * 148 * 2048;
+    const unsigned grid4 = blocks(((int64_t)batch->tokens + 3) / 4 * cache->kv_heads, L);
     return by_type(dtype, [&](auto t) {
       using T = decltype(t);
-      if (cache->format == DG_KV_E4M3) k_cache_read<T, L, true><<<grid, THREADS, 0, (cudaStream_t)stream>>>(a);
-      else k_cache_read<T, L, false><<<grid, THREADS, 0, (cudaStream_t)stream>>>(a);
+      cudaStream_t s = (cudaStream_t)stream;
+      if (cache->format == DG_KV_E4M3) {
+        if (many) k_cache_read<T, L, true, 4><<<grid4, THREADS, 0, s>>>(a);
+        else k_cache_read<T, L, true, 1><<<grid, THREADS, 0, s>>>(a);
+      } else {
+        if (many) k_cache_read<T, L, false, 4><<<grid4, THREADS, 0, s>>>(a);
+        else k_cache_read<T, L, false, 1><<<grid, THREADS, 0, s>>>(a);
+      }
       return cudaGetLastError();
     });
   }));
