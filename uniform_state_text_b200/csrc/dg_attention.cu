@@ -1193,9 +1193,13 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
 }
 
 // Joins the pieces of the items that lie in more than one CTA's share. The
-// rows of all such items form one list that the blocks take turns at; a row's
-// pieces are divided over 2, 4 or 8 warps and added in a fixed order, so that
-// the result does not depend on timing.
+// rows of all such items form one list that the blocks take turns at: a warp per
+// row, or all eight where a row has more than kFewPieces. A row's pieces are
+// added in a fixed order, so that the result does not depend on timing. Bound by
+// the latency of three dependent loads (which item, its maxima, its sums); a
+// block per row and piece, as it first was, took three times as long.
+constexpr int kFewPieces = 16;
+
 template <class S>
 __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Args a, int ctas) {
   constexpr int V = S::DP / 32;                       // columns per lane
@@ -1207,17 +1211,12 @@ __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Args a, in
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x < ctas) open_s[threadIdx.x] = a.open[threadIdx.x];
   __syncthreads();
-  // warps per row, and units (groups of 8 / per rows) of an item
-  auto per_of = [](int pieces) { return pieces > 4 ? 8 : pieces > 2 ? 4 : 2; };
   if (warp == 0) {
     int run = 0;
     for (int b0 = 0; b0 < ctas; b0 += 32) {
       const int at = b0 + lane;
       int u = 0;
-      if (at < ctas && open_s[at].rows) {
-        const int group = 8 / per_of(open_s[at].pieces);
-        u = (open_s[at].rows + group - 1) / group;
-      }
+      if (at < ctas) u = open_s[at].pieces > kFewPieces ? open_s[at].rows : (open_s[at].rows + 7) / 8;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, u, d);
@@ -1229,7 +1228,6 @@ __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Args a, in
     if (lane == 0) upto[0] = 0;
   }
   __syncthreads();
-  const int D = a.w.c.head_dim;
   for (int unit = blockIdx.x; unit < upto[ctas]; unit += gridDim.x) {
     int lo = 0, hi = ctas;                            // upto[lo] <= unit < upto[hi]
     while (hi - lo > 1) {
@@ -1237,60 +1235,70 @@ __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Args a, in
       if (upto[mid] <= unit) lo = mid;
       else hi = mid;
     }
-    const Open& op = open_s[lo];
-    const int per = per_of(op.pieces), sub = warp % per;
-    const int r = (unit - upto[lo]) * (8 / per) + warp / per;
-    float m = -INFINITY, l = 0.f, o[V];
+    const Open op = open_s[lo];
+    const bool few = op.pieces <= kFewPieces;         // the same for the whole block
+    const int r = (unit - upto[lo]) * (few ? 8 : 1) + (few ? warp : 0);
+    const int first = few ? 0 : warp, step = few ? 1 : 8;
+    const int n = r < op.rows ? (op.pieces - first + step - 1) / step : 0;   // this warp's pieces, at most 19
+    auto place = [&](int k) {                         // of its k-th
+      const int p = first + k * step;
+      return (int64_t)((lo + p) * 2 + (p == 0 ? 1 : 0)) * a.rows + r;
+    };
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < n) ml = a.part_ml[place(lane)];
+    float m = ml.x;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float f = ex2(ml.x - (m == -INFINITY ? 0.f : m));
+    float l = lane < n ? f * ml.y : 0.f;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    float o[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) o[k] = 0.f;
-    if (r < op.rows) {
 #pragma unroll 4
-      for (int p = sub; p < op.pieces; p += per) {
-        const int64_t at = (int64_t)((lo + p) * 2 + (p == 0 ? 1 : 0)) * a.rows + r;
-        const float2 ml = a.part_ml[at];
-        const float* src = a.part_o + at * S::DP + lane * V;
-        float v[V];
+    for (int k = 0; k < n; ++k) {
+      const float* src = a.part_o + place(k) * S::DP + lane * V;
+      const float g = __shfl_sync(0xffffffffu, f, k);
 #pragma unroll
-        for (int k = 0; k < V; k += 2) {
-          const float2 f = *reinterpret_cast<const float2*>(src + k);
-          v[k] = f.x;
-          v[k + 1] = f.y;
+      for (int c = 0; c < V; c += 2) {
+        const float2 x = *reinterpret_cast<const float2*>(src + c);
+        o[c] = fmaf(x.x, g, o[c]);
+        o[c + 1] = fmaf(x.y, g, o[c + 1]);
+      }
+    }
+    if (!few) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) o_s[warp][lane * V + k] = o[k];
+      if (lane == 0) { m_s[warp] = m; l_s[warp] = l; }
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int p = 1; p < 8; ++p) m = fmaxf(m, m_s[p]);
+        const float base = m == -INFINITY ? 0.f : m;
+        l = 0.f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) o[k] = 0.f;
+        for (int p = 0; p < 8; ++p) {
+          const float g = ex2(m_s[p] - base);
+          l += g * l_s[p];
+#pragma unroll
+          for (int k = 0; k < V; ++k) o[k] = fmaf(o_s[p][lane * V + k], g, o[k]);
         }
-        const float mn = fmaxf(m, ml.x);
-        const float base = mn == -INFINITY ? 0.f : mn;
-        const float f0 = ex2(m - base), f1 = ex2(ml.x - base);
-        l = l * f0 + ml.y * f1;
-#pragma unroll
-        for (int k = 0; k < V; ++k) o[k] = o[k] * f0 + v[k] * f1;
-        m = mn;
       }
+      __syncthreads();
+      if (warp) continue;
     }
+    if (n == 0) continue;
+    const uint32_t rid = (uint32_t)op.m * (S::NT * 128) + r;
+    const uint32_t i = a.over_g(rid), g = rid - i * (uint32_t)a.G;
+    const int64_t orow = (int64_t)(op.t0 + i) * a.q_heads + op.h * a.G + g;
+    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
 #pragma unroll
-    for (int k = 0; k < V; ++k) o_s[warp][lane * V + k] = o[k];
-    if (lane == 0) { m_s[warp] = m; l_s[warp] = l; }
-    __syncthreads();
-    if (sub == 0 && r < op.rows) {
-      for (int p = 1; p < per; ++p) {
-        const float pm = m_s[warp + p], pl = l_s[warp + p];
-        const float mn = fmaxf(m, pm);
-        const float base = mn == -INFINITY ? 0.f : mn;
-        const float f0 = ex2(m - base), f1 = ex2(pm - base);
-        l = l * f0 + pl * f1;
-#pragma unroll
-        for (int k = 0; k < V; ++k) o[k] = o[k] * f0 + o_s[warp + p][lane * V + k] * f1;
-        m = mn;
-      }
-      const uint32_t rid = (uint32_t)op.m * (S::NT * 128) + r;
-      const uint32_t i = a.over_g(rid), g = rid - i * (uint32_t)a.G;
-      const int64_t orow = (int64_t)(op.t0 + i) * a.q_heads + op.h * a.G + g;
-      const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-#pragma unroll
-      for (int k = 0; k < V; k += 2)
-        if (lane * V + k < D)
-          *reinterpret_cast<uint32_t*>(a.out + orow * D + lane * V + k) = pack_bf16(o[k] * inv, o[k + 1] * inv);
-      if (lane == 0 && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-    }
-    __syncthreads();
+    for (int k = 0; k < V; k += 2)
+      if (lane * V + k < a.w.c.head_dim)
+        *reinterpret_cast<uint32_t*>(a.out + orow * a.w.c.head_dim + lane * V + k) = pack_bf16(o[k] * inv, o[k + 1] * inv);
+    if (lane == 0 && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 
@@ -1343,9 +1351,8 @@ cudaError_t launch(Args a, int ctas, cudaStream_t s) {
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  // a row per block at least, at most four blocks per SM: whatever the lengths,
-  // no more than ctas - 1 items are cut
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(4ll * ctas, (int64_t)(ctas - 1) * a.rows));
+  // no more than ctas - 1 items are cut, whatever the lengths; as many blocks as fit at once
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(6ll * ctas, (int64_t)(ctas - 1) * a.rows));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cfg.attrs = at;
