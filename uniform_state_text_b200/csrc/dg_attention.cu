@@ -86,6 +86,7 @@ struct Args {
   struct Open* open;           // [CTAs] the item a CTA begins and does not finish
   int rows;                    // rows kept per piece
   int box;                     // rows per TMA copy: a power of two that divides page_size; 0: no TMA
+  int q_box;                   // queries by TMA, 32 rows (32 / G tokens of G heads) at a time
 
   __device__ __forceinline__ uint32_t over_g(uint32_t r) const {
     return (uint32_t)(((uint64_t)r * g_mul) >> g_shift);
@@ -565,6 +566,29 @@ __device__ __forceinline__ void load_queries(const W& w, int part, uint32_t dst)
   copies_landed();
 }
 
+// The same by TMA, one warp for all: a row r of an item is token r / G, head
+// r % G, so that G heads of 32 / G tokens, as a box takes them, are 32 rows in
+// order. (Rows behind the sequence's last hold the next one's, or zeros; no
+// other row's result depends on them.)
+template <class S, typename W>
+__device__ __forceinline__ void query_boxes(const W& w, const CUtensorMap* map, uint32_t dst, uint64_t* bar) {
+  constexpr int NB = S::DP / 64, ROWS = S::NT * 128;
+  const int lane = threadIdx.x & 31, rows = w.rows();
+  const bool few = S::FEW && rows <= 32;
+  const int group = lane / NB, cb = lane % NB, n = few ? 4 : (rows + 31) / 32;   // groups of 32 rows
+  if (lane == 0) mbar_expect_tx(bar, n * NB * 32 * 128);
+  __syncwarp();
+  if (group < n) {
+    const uint32_t i = w.a.over_g((uint32_t)w.m * ROWS + (few ? 0 : group * 32));
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            dst + (group >> 2) * S::QTILE + cb * (128 * 128) + (group & 3) * (32 * 128)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(cb * 64), "r"(w.h * w.a.G), "r"(w.t0 + (int)i)
+        : "memory");
+  }
+  __syncwarp();
+}
+
 // e4m3: rows r0 to r0 + BN / CW of a tile of codes to bf16 in a ring slot.
 template <class S>
 __device__ __forceinline__ void convert(const uint8_t* exps, int r0, uint32_t src, uint32_t slot) {
@@ -688,7 +712,8 @@ __device__ __forceinline__ void transpose4(uint4* v) {
 // end of the item.
 template <class S>
 __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap k_map,
-                                                           const __grid_constant__ CUtensorMap v_map) {
+                                                           const __grid_constant__ CUtensorMap v_map,
+                                                           const __grid_constant__ CUtensorMap q_map) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -710,7 +735,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       mbar_init(&sy.o_done[x], 1);
       mbar_init(&sy.o_free[x], 4);
     }
-    mbar_init(&sy.q_full, S::N_LOAD);
+    mbar_init(&sy.q_full, a.q_box ? 1 : S::N_LOAD);
     mbar_init(&sy.q_free, 1);
     mbar_init(&sy.fin, 1);
     mbar_init(&sy.merge, 4);
@@ -995,13 +1020,26 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     bool ok = true;
     Pages pages;
     uint32_t e = 0, e0 = 0, seg = 0;                  // ring entry; the segment's first, tile tb's keys; segments
+    bool q_landing = false;                           // this warp brings the queries by TMA; the last copy's phase
+    uint32_t q_phase = 0;
     auto queries = [&]() {
+      if (a.q_box && part) return true;
       if (seg && !__all_sync(0xffffffffu, wait(&sy.q_free, (seg - 1) & 1, sy, a))) return false;
+      if (a.q_box) {
+        query_boxes<S>(w, &q_map, smem_u32(smem), &sy.q_full);
+        q_landing = true;
+        q_phase = seg & 1;
+        return true;
+      }
       load_queries<S>(w, part, smem_u32(smem));
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sy.q_full);
       return true;
+    };
+    // a CTA that gives up still waits for its last copies
+    auto drain_queries = [&]() {
+      if (q_landing) wait(&sy.q_full, q_phase, sy, a, false);
     };
     auto position = [&]() { return (int64_t)(w.tb + (int)((e - e0) >> 1)) * BN; };
     auto to_clean = [&]() {                           // values that not every row of the item sees
@@ -1041,7 +1079,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
         }
         e0 += n;
       }
-      // a CTA that gives up still waits for its last copies
+      drain_queries();
       if (landing) wait(&sy.full[part], (e / S::SL - 1) & 1, sy, a, false);
     } else if (warp == S::W_FETCH) {
       // codes and exponents, AHEAD tiles before they are converted
@@ -1099,6 +1137,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
         }
         e0 += n;
       }
+      drain_queries();
     }
   } else {
     // ---------------------------------------------------------------- MMA
@@ -1342,9 +1381,19 @@ cudaError_t launch(Args a, int ctas, cudaStream_t s) {
   if (a.box && (!tc_encode_2d_rows(&maps[0], c.k, c.head_dim, rows, 64, a.box, S::F8) ||
                 !tc_encode_2d_rows(&maps[1], c.v, c.head_dim, rows, 64, a.box, S::F8)))
     return cudaErrorInvalidValue;
+  // queries: dimensions (column, head, token); a dimension of one takes any stride
+  const int64_t hs = a.q_heads > 1 ? a.q_hs : c.head_dim, ts = a.w.b.tokens > 1 ? a.q_ts : a.q_heads * hs;
+  a.q_box = a.G <= 32 && !(a.G & (a.G - 1)) && c.head_dim >= 64 && hs > 0 && ts > 0 && hs < (1ll << 38) && ts < (1ll << 38);
+  alignas(64) CUtensorMap q_map = {};
+  if (a.q_box) {
+    const uint64_t dims[3] = {(uint64_t)c.head_dim, (uint64_t)a.q_heads, (uint64_t)a.w.b.tokens};
+    const uint64_t strides[2] = {2 * (uint64_t)hs, 2 * (uint64_t)ts};
+    const uint32_t box[3] = {64, (uint32_t)a.G, 32 / (uint32_t)a.G};
+    if (!tc_encode_3d_bf16(&q_map, a.q, dims, strides, box)) return cudaErrorInvalidValue;
+  }
   cudaError_t e = cudaFuncSetAttribute(k_attend<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
   if (e != cudaSuccess) return e;
-  k_attend<S><<<ctas, S::THREADS, S::SMEM, s>>>(a, maps[0], maps[1]);
+  k_attend<S><<<ctas, S::THREADS, S::SMEM, s>>>(a, maps[0], maps[1], q_map);
   if ((e = cudaGetLastError()) != cudaSuccess || ctas == 1) return e;
   // the join's launch overlaps the kernel's end; it waits for it on the device
   cudaLaunchAttribute at[1];
@@ -1419,7 +1468,7 @@ extern "C" int dg_cache_attention(const dg_kv_cache* cache, const dg_kv_batch* b
   const Args a{{*cache, *batch}, static_cast<const __nv_bfloat16*>(q), q_ts, q_hs, q_heads,
                (int)G, mul, 31 + log, scale * 1.4426950408889634f, mask, tree_mask, mask_words,
                static_cast<__nv_bfloat16*>(out), lse, reinterpret_cast<float*>(sc + p.o),
-               reinterpret_cast<float2*>(sc + p.ml), reinterpret_cast<Open*>(sc + p.open), p.rows, 0};
+               reinterpret_cast<float2*>(sc + p.ml), reinterpret_cast<Open*>(sc + p.open), p.rows, 0, 0};
   const int ctas = std::min(sms, kMaxCtas);
   const bool f8 = cache->format == DG_KV_E4M3;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

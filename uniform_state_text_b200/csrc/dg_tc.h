@@ -37,6 +37,9 @@ bool tc_encode_2d_bf16(void* map, const void* base, uint64_t inner, uint64_t out
 // the cache's pages.
 bool tc_encode_2d_rows(void* map, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
                        uint32_t box_outer, bool bytes);
+// A 3-D map of bf16 (128-byte swizzle): dims and box innermost first, strides in
+// bytes of dimensions 1 and 2.
+bool tc_encode_3d_bf16(void* map, const void* base, const uint64_t* dims, const uint64_t* strides, const uint32_t* box);
 // tc_supported, and the current device has SMs enough for both CTA roles.
 bool tc_fits_device(int C, int V, int d);
 // The work split tc_layout picks on a GPU with `sms` SMs, in the order
