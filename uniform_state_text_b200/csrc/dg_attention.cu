@@ -319,6 +319,13 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Sync& sy, c
   return mbar_try(bar, parity) || wait_slow(bar, parity, &sy.abort, a.w.c.status, check_abort);
 }
 
+// A whole warp waits, every lane for itself: with one lane waiting and the others
+// held until it had, each hand-over took several times as long (the whole kernel
+// up to twice), so no role waits in a divergent warp.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Sync& sy, const Args& a) {
+  return __all_sync(0xffffffffu, wait(bar, parity, sy, a)) != 0;
+}
+
 // D (TMEM) += A (TMEM, bf16) B (shared memory).
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -338,6 +345,29 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// The same in two halves: the issue (its registers are not to be read yet), and
+// the wait, which names them so that no read moves above it.
+__device__ __forceinline__ void tmem_ld16_issue(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+// 8 registers of each lane to 8 columns of TMEM.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 // 16 registers of each lane to 16 columns of TMEM.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
@@ -368,6 +398,49 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t src) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "r"(src) : "memory");
   return v;
+}
+// Pairs of floats in one register pair, and the instructions that work on both.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi2(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {   // NaN if one of them is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t exp2_mufu2(uint64_t x) { return pack2(ex2(lo2(x)), ex2(hi2(x))); }
+// 2^x without the special-function unit, of which an SM has 16 lanes to 128 for
+// arithmetic: x = n + f with n the nearest whole number (by adding 1.5 2^23),
+// 2^f on [-1/2, 1/2] by the polynomial of degree 5 through 2^f at the Chebyshev
+// points (relative error 2.1e-7 in fp32), n added to the exponent. For x from
+// -126 (smaller ones give 2^-126) to 127, not NaN.
+__device__ __forceinline__ uint64_t exp2_poly2(uint64_t x) {
+  constexpr float kMagic = 12582912.0f;
+  x = pack2(fmaxf(lo2(x), -126.0f), fmaxf(hi2(x), -126.0f));
+  const uint64_t r = add2(x, pack2(kMagic, kMagic));
+  const uint64_t f = fma2(add2(r, pack2(-kMagic, -kMagic)), pack2(-1.f, -1.f), x);
+  uint64_t p = pack2(0.00133908633f, 0.00133908633f);
+  p = fma2(p, f, pack2(0.00967603177f, 0.00967603177f));
+  p = fma2(p, f, pack2(0.0555035695f, 0.0555035695f));
+  p = fma2(p, f, pack2(0.240221068f, 0.240221068f));
+  p = fma2(p, f, pack2(0.693147182f, 0.693147182f));
+  p = fma2(p, f, pack2(1.00000012f, 1.00000012f));
+  return pack2(__uint_as_float((uint32_t)p + ((uint32_t)r << 23)),
+               __uint_as_float((uint32_t)(p >> 32) + ((uint32_t)(r >> 32) << 23)));
 }
 // Byte offset of 16-byte chunk c (8 bf16 columns) of row r in an operand tile of
 // `rows` rows: blocks of 64 columns, 128-byte rows, the chunk index xored with r % 8.
@@ -772,7 +845,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     // NT = 2, but only after that of k - 2 with NT = 1, which therefore
     // alternates between two barriers.
     auto pv_done = [&](uint32_t k) {
-      return S::NT == 2 ? wait(&sy.o_done[x], k & 1, sy, a) : wait(&sy.o_done[k & 1], (k >> 1) & 1, sy, a);
+      return S::NT == 2 ? wait_warp(&sy.o_done[x], k & 1, sy, a) : wait_warp(&sy.o_done[k & 1], (k >> 1) & 1, sy, a);
     };
     Open open{0, 0, 0, 0, 0};                         // an item begun and not finished
     uint32_t merges = 0;
@@ -791,16 +864,39 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       for (int t = w.tb; t < w.te; ++t, ++gt) {
         const int buf = S::NT == 2 ? x : (int)(gt & 1);
         const uint32_t ph = S::NT == 2 ? gt & 1 : (gt >> 1) & 1;
-        if (!__all_sync(0xffffffffu, wait(&sy.s_full[buf], ph, sy, a))) { ok = false; break; }
+        if (!wait_warp(&sy.s_full[buf], ph, sy, a)) { ok = false; break; }
         if (any) {
           tc_fence_after();
           const uint32_t t_s = tmem + buf * S::T_S + lanes;
           const int64_t j0 = (int64_t)t * BN;
           const bool masked = __any_sync(0xffffffffu, j0 + BN > clear);
-          // chunks of 32 columns: all of them, or this warp's own
-          const int c0 = few ? quarter : 0, c1 = few ? quarter + 1 : BN / 32;
-          float s[32];
+          // The usual tile, all columns seen: straight code, the next 16 columns on
+          // their way from TMEM while one chunk is worked on.
+          bool plain = !masked && !few;
+          uint32_t ra[16], rb[16];
           float top = -INFINITY;
+          if (plain) {
+            tmem_ld16_issue(t_s, ra);
+#pragma unroll
+            for (int c = 0; c < BN / 16; ++c) {
+              uint32_t* r = c & 1 ? rb : ra;
+              tmem_ld16_wait(r);
+              if (c + 1 < BN / 16) tmem_ld16_issue(t_s + (c + 1) * 16, c & 1 ? ra : rb);
+              float u0 = top, u1 = __uint_as_float(r[15]);
+#pragma unroll
+              for (int j = 0; j < 14; j += 4) {
+                u0 = max3_nan(u0, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+                if (j + 3 < 15) u1 = max3_nan(u1, __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
+                else u1 = max3_nan(u1, __uint_as_float(r[j + 2]), u1);
+              }
+              top = max3_nan(u0, u1, u1);
+            }
+            plain = !__any_sync(0xffffffffu, top != top && valid);    // NaN: below, where it goes by MUFU
+          }
+          // chunks of 32 columns: all of them, or this warp's own
+          const int c0 = few ? quarter : 0, c1 = plain ? c0 : few ? quarter + 1 : BN / 32;
+          float s[32];
+          if (!plain) top = -INFINITY;
 #pragma unroll 1
           for (int c = c0; c < c1; ++c) {
             tmem_ld32(t_s + c * 32, s);
@@ -822,7 +918,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           const bool first = t == w.tb;
           const bool move = top > m + kGrow || (m == -INFINITY && top > m);
           if (!first && __any_sync(0xffffffffu, move && valid)) {
-            if (!__all_sync(0xffffffffu, pv_done(gt - 1))) { ok = false; break; }
+            if (!pv_done(gt - 1)) { ok = false; break; }
             tc_fence_after();
             const float f = move ? ex2(m - top) : 1.f;
             l *= f;
@@ -841,6 +937,28 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           if (move) m = top;
           const float sub = m == -INFINITY ? 0.f : m;  // a row that has seen nothing yet: P = 0
           float l0 = 0.f, l1 = 0.f;
+          if (plain) {
+            const uint64_t sc = pack2(a.scale_log2, a.scale_log2), ns = pack2(-sub, -sub);
+            uint64_t ls = pack2(0.f, 0.f);
+            tmem_ld16_issue(t_s, ra);
+#pragma unroll
+            for (int c = 0; c < BN / 16; ++c) {
+              uint32_t* r = c & 1 ? rb : ra;
+              tmem_ld16_wait(r);
+              if (c + 1 < BN / 16) tmem_ld16_issue(t_s + (c + 1) * 16, c & 1 ? ra : rb);
+              uint32_t p[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const uint64_t x = fma2(pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), sc, ns);
+                const uint64_t e = (j & 3) == 3 ? exp2_poly2(x) : exp2_mufu2(x);
+                ls = add2(ls, e);
+                p[j] = pack_bf16(lo2(e), hi2(e));
+              }
+              tmem_st8(t_s + c * 8, p);
+            }
+            l0 = lo2(ls);
+            l1 = hi2(ls);
+          }
 #pragma unroll 1
           for (int c = c0; c < c1; ++c) {
             if (!few) {                               // one chunk is still in registers
@@ -876,7 +994,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       }
       if (!ok) break;
       // ---------------------------------------------------------- the segment's result
-      if (!__all_sync(0xffffffffu, pv_done(gt - 1))) { ok = false; break; }
+      if (!pv_done(gt - 1)) { ok = false; break; }
       const bool whole = w.tb == 0 && w.te == w.T;
       const bool fix = a.mask != DG_MASK_FULL && *(volatile int*)&sy.nonfinite;
       const int piece = blockIdx.x * 2 + (w.tb == 0 ? 1 : 0);
@@ -889,7 +1007,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
         auto meet = [&]() {
           __syncwarp();
           if (lane == 0) mbar_arrive(&sy.merge);
-          return __all_sync(0xffffffffu, wait(&sy.merge, merges++ & 1, sy, a)) != 0;
+          return wait_warp(&sy.merge, merges++ & 1, sy, a);
         };
         few_ml[quarter * 32 + lane] = make_float2(m, l);
         if (!meet()) { ok = false; break; }
@@ -1024,7 +1142,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     uint32_t q_phase = 0;
     auto queries = [&]() {
       if (a.q_box && part) return true;
-      if (seg && !__all_sync(0xffffffffu, wait(&sy.q_free, (seg - 1) & 1, sy, a))) return false;
+      if (seg && !wait_warp(&sy.q_free, (seg - 1) & 1, sy, a)) return false;
       if (a.q_box) {
         query_boxes<S>(w, &q_map, smem_u32(smem), &sy.q_full);
         q_landing = true;
@@ -1064,7 +1182,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           int eight, row[BN / 32];
           const bool boxes = find_eights<S>(w, pages, position(), &eight) && !clean;   // under the wait for the slot
           if (!boxes) find_rows<S>(w, position(), row);
-          if (!__all_sync(0xffffffffu, wait(&sy.empty[part], ((e / S::SL) & 1) ^ 1, sy, a))) { ok = false; break; }
+          if (!wait_warp(&sy.empty[part], ((e / S::SL) & 1) ^ 1, sy, a)) { ok = false; break; }
           landing = boxes;
           if (boxes) {                                // the copies arrive on `full` themselves
             copy_boxes<S>(a, kv ? &v_map : &k_map, eight, dst, &sy.full[part]);
@@ -1092,7 +1210,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           int eight, row[BN / 32];
           const bool boxes = find_eights<S>(w, pages, position(), &eight);    // under the wait for the buffer
           if (!boxes) find_rows<S>(w, position(), row);
-          if (!__all_sync(0xffffffffu, wait(&sy.taken[at], ((e / S::AHEAD) & 1) ^ 1, sy, a))) { ok = false; break; }
+          if (!wait_warp(&sy.taken[at], ((e / S::AHEAD) & 1) ^ 1, sy, a)) { ok = false; break; }
           if (boxes) {
             copy_boxes<S>(a, kv ? &v_map : &k_map, eight, dst, &sy.raw[at]);
             if (eight >= 0)
@@ -1122,8 +1240,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
         const uint32_t n = 2 * (uint32_t)(w.te - w.tb);
         for (; e - e0 < n; ++e) {
           const uint32_t at = e % S::AHEAD, slot = e % S::SL, dst = ring0 + slot * S::SLOT;
-          if (!__all_sync(0xffffffffu, wait(&sy.raw[at], (e / S::AHEAD) & 1, sy, a)) ||
-              !__all_sync(0xffffffffu, wait(&sy.empty[slot], ((e / S::SL) & 1) ^ 1, sy, a))) { ok = false; break; }
+          if (!wait_warp(&sy.raw[at], (e / S::AHEAD) & 1, sy, a) ||
+              !wait_warp(&sy.empty[slot], ((e / S::SL) & 1) ^ 1, sy, a)) { ok = false; break; }
           convert<S>(sy.exps[at], r0, codes0 + at * S::RAW, dst);
           if (to_clean()) clean_rows<S, RW>(dst, r0, sy);
           fence_async_shared();
@@ -1141,17 +1259,16 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     }
   } else {
     // ---------------------------------------------------------------- MMA
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16(128, BN, 0), id_o = idesc_bf16(128, S::DP, 1);
-      const uint32_t q0 = smem_u32(smem), ring0 = smem_u32(ring);
-      uint32_t e = 0, gt = 0, seg = 0;                // ring entries, key tiles and segments so far
-      bool ok = true;
-      auto slot_full = [&](uint32_t entry) {
-        if (!wait(&sy.full[entry % S::SL], (entry / S::SL) & 1, sy, a)) return false;
-        tc_fence_after();
-        return true;
-      };
-      auto scores = [&](uint32_t entry, int x, int buf) {   // S(buf) = Q(x) K^T
+    // (the warp waits together, lane 0 issues)
+    constexpr uint32_t id_s = idesc_bf16(128, BN, 0), id_o = idesc_bf16(128, S::DP, 1);
+    const uint32_t q0 = smem_u32(smem), ring0 = smem_u32(ring);
+    uint32_t e = 0, gt = 0, seg = 0;                  // ring entries, key tiles and segments so far
+    bool ok = true;
+    auto slot_full = [&](uint32_t entry) { return wait_warp(&sy.full[entry % S::SL], (entry / S::SL) & 1, sy, a); };
+    auto commit = [&](uint64_t* bar) { if (lane == 0) mma_commit(bar); };
+    auto scores = [&](uint32_t entry, int x, int buf) {   // S(buf) = Q(x) K^T
+      tc_fence_after();
+      if (lane == 0) {
         const uint32_t k0 = ring0 + (entry % S::SL) * S::SLOT;
 #pragma unroll
         for (int k = 0; k < S::DP / 16; ++k)
@@ -1159,67 +1276,69 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
                    sdesc(q0 + x * S::QTILE + (k >> 2) * (128 * 128) + (k & 3) * 32, 16, 1024),
                    sdesc(k0 + (k >> 2) * (BN * 128) + (k & 3) * 32, 16, 1024), id_s, k ? 1u : 0u);
         mma_commit(&sy.s_full[buf]);
-      };
-      auto sums = [&](uint32_t entry, int x, int buf, bool first) {   // O(x) += P(buf) V
+      }
+    };
+    auto sums = [&](uint32_t entry, int x, int buf, bool first) {   // O(x) += P(buf) V
+      tc_fence_after();
+      if (lane == 0) {
         const uint32_t v0 = ring0 + (entry % S::SL) * S::SLOT;
 #pragma unroll
         for (int k = 0; k < BN / 16; ++k)
           mma_bf16_ts(tmem + S::T_O + x * S::DP, tmem + buf * S::T_S + k * 8,
                       sdesc(v0 + k * 2048, BN * 128, 1024), id_o, first && k == 0 ? 0u : 1u);
         mma_commit(&sy.o_done[S::NT == 2 ? x : buf]);
-      };
-      for (; w.more() && ok; w.next(), ++seg) {
-        if (!wait(&sy.q_full, seg & 1, sy, a) || !slot_full(e)) { ok = false; break; }
-        const int n = w.te - w.tb;
-        if constexpr (S::NT == 2) {
-          scores(e, 0, 0);
-          scores(e, 1, 1);
-          mma_commit(&sy.empty[e % S::SL]);
-          if (n == 1) mma_commit(&sy.q_free);
-          for (int t = 0; t < n && ok; ++t, ++gt, e += 2) {
-            for (int x = 0; x < 2; ++x) {
-              if (!wait(&sy.p_full[x], gt & 1, sy, a) ||
-                  (t == 0 && seg && !wait(&sy.o_free[x], (seg - 1) & 1, sy, a)) ||
-                  (x == 0 && !slot_full(e + 1))) { ok = false; break; }
-              tc_fence_after();
-              sums(e + 1, x, x, t == 0);
-              if (x == 1) mma_commit(&sy.empty[(e + 1) % S::SL]);
-              if (t + 1 < n) {
-                if (x == 0 && !slot_full(e + 2)) { ok = false; break; }
-                scores(e + 2, x, x);
-                if (x == 1) {
-                  mma_commit(&sy.empty[(e + 2) % S::SL]);
-                  if (t + 2 == n) mma_commit(&sy.q_free);
-                }
+      }
+    };
+    for (; w.more() && ok; w.next(), ++seg) {
+      if (!wait_warp(&sy.q_full, seg & 1, sy, a) || !slot_full(e)) { ok = false; break; }
+      const int n = w.te - w.tb;
+      if constexpr (S::NT == 2) {
+        scores(e, 0, 0);
+        scores(e, 1, 1);
+        commit(&sy.empty[e % S::SL]);
+        if (n == 1) commit(&sy.q_free);
+        for (int t = 0; t < n && ok; ++t, ++gt, e += 2) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!wait_warp(&sy.p_full[x], gt & 1, sy, a) ||
+                (t == 0 && seg && !wait_warp(&sy.o_free[x], (seg - 1) & 1, sy, a)) ||
+                (x == 0 && !slot_full(e + 1))) { ok = false; break; }
+            sums(e + 1, x, x, t == 0);
+            if (x == 1) commit(&sy.empty[(e + 1) % S::SL]);
+            if (t + 1 < n) {
+              if (x == 0 && !slot_full(e + 2)) { ok = false; break; }
+              scores(e + 2, x, x);
+              if (x == 1) {
+                commit(&sy.empty[(e + 2) % S::SL]);
+                if (t + 2 == n) commit(&sy.q_free);
               }
             }
           }
-        } else {
-          scores(e, 0, gt & 1);
-          mma_commit(&sy.empty[e % S::SL]);
-          if (n == 1) mma_commit(&sy.q_free);
-          for (int t = 0; t < n && ok; ++t, ++gt, e += 2) {
-            if (t + 1 < n) {
-              if (!slot_full(e + 2)) { ok = false; break; }
-              scores(e + 2, 0, (gt + 1) & 1);
-              mma_commit(&sy.empty[(e + 2) % S::SL]);
-              if (t + 2 == n) mma_commit(&sy.q_free);
-            }
-            if (!wait(&sy.p_full[gt & 1], (gt >> 1) & 1, sy, a) ||
-                (t == 0 && seg && !wait(&sy.o_free[0], (seg - 1) & 1, sy, a)) || !slot_full(e + 1)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            sums(e + 1, 0, gt & 1, t == 0);
-            mma_commit(&sy.empty[(e + 1) % S::SL]);
+        }
+      } else {
+        scores(e, 0, gt & 1);
+        commit(&sy.empty[e % S::SL]);
+        if (n == 1) commit(&sy.q_free);
+        for (int t = 0; t < n && ok; ++t, ++gt, e += 2) {
+          if (t + 1 < n) {
+            if (!slot_full(e + 2)) { ok = false; break; }
+            scores(e + 2, 0, (gt + 1) & 1);
+            commit(&sy.empty[(e + 2) % S::SL]);
+            if (t + 2 == n) commit(&sy.q_free);
           }
+          if (!wait_warp(&sy.p_full[gt & 1], (gt >> 1) & 1, sy, a) ||
+              (t == 0 && seg && !wait_warp(&sy.o_free[0], (seg - 1) & 1, sy, a)) || !slot_full(e + 1)) {
+            ok = false;
+            break;
+          }
+          sums(e + 1, 0, gt & 1, t == 0);
+          commit(&sy.empty[(e + 1) % S::SL]);
         }
       }
-      // every MMA issued has completed before TMEM is released and the CTA exits
-      mma_commit(&sy.fin);
-      wait(&sy.fin, 0, sy, a, false);
     }
+    // every MMA issued has completed before TMEM is released and the CTA exits
+    commit(&sy.fin);
+    wait(&sy.fin, 0, sy, a, false);
     __syncwarp();
   }
   copies_landed();
