@@ -119,8 +119,8 @@ struct Shape {
   static constexpr bool FEW = NT == 1 && BN == 128;
   static constexpr int W_LOAD = NT * 4, W_FETCH = W_LOAD + N_LOAD, W_MMA = W_FETCH + (F8 ? 1 : 0);
   static constexpr int THREADS = (W_MMA + 1) * 32;
-  static constexpr int T_S = NT == 2 ? 128 : BN;       // TMEM columns between S buffers
-  static constexpr int T_O = NT == 2 ? 256 : 2 * BN;   // first column of O
+  // TMEM: two S buffers, tile x's (NT = 2) or key tile k's (NT = 1, k mod 2); then O
+  static constexpr int T_O = 2 * BN;
   static constexpr size_t SMEM = 1024 + (size_t)NT * QTILE + (size_t)SL * SLOT + (size_t)AHEAD * RAW + (FEW ? 4 * 32 * 64 + 4 * 32 * 8 : 0) + 1024;
   static_assert(8 * (kMaxBatch + 1) <= SL * SLOT, "the plan's sums lie in the ring before it is used");
   static_assert(T_O + NT * DP <= TMEM_COLS, "TMEM");
@@ -285,9 +285,12 @@ __device__ __forceinline__ void begin(Walk<ROWS, BN>& w, const Start& st) {
 // Small pieces.
 // ---------------------------------------------------------------------------
 struct Sync {
-  uint64_t full[8], empty[8];      // ring slots
-  uint64_t s_full[2], p_full[2];   // S ready; P stored
-  uint64_t o_done[2], o_free[2];   // P V done; O read
+  // Barriers of a key tile k lie at k mod 4, with phase k / 4: whoever waits may
+  // then be up to four tiles behind (a parity wait on a barrier that has gone on
+  // by two phases, or not yet reached the one before, answers for another phase).
+  uint64_t full[8];                // ring slots
+  uint64_t s_full[8], p_full[8];   // 4 x + k mod 4: S ready (the keys' slot is free after the last x), P stored
+  uint64_t o_done[8], o_free[2];   // P V done (the values' slot is free after the last x); O read
   uint64_t q_full, q_free, fin;
   uint64_t raw[4], taken[4];       // e4m3: a tile's codes have landed, and have been converted
   uint8_t exps[4][128];            // their rows' exponents
@@ -801,12 +804,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S::SL; ++s) { mbar_init(&sy.full[s], S::F8 ? S::CW : 1); mbar_init(&sy.empty[s], 1); }
-    for (int x = 0; x < 2; ++x) {
+    for (int s = 0; s < S::SL; ++s) mbar_init(&sy.full[s], S::F8 ? S::CW : 1);
+    for (int x = 0; x < 8; ++x) {
       mbar_init(&sy.s_full[x], 1);
       mbar_init(&sy.p_full[x], 4);
       mbar_init(&sy.o_done[x], 1);
-      mbar_init(&sy.o_free[x], 4);
+      if (x < 2) mbar_init(&sy.o_free[x], 4);
     }
     mbar_init(&sy.q_full, a.q_box ? 1 : S::N_LOAD);
     mbar_init(&sy.q_free, 1);
@@ -840,13 +843,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     const uint32_t t_o = tmem + S::T_O + x * S::DP + lanes;
     bool ok = true;
     uint32_t gt = 0;                                  // key tiles done by this CTA
-    // P V of key tile k is complete. A parity wait must not start two phases
-    // ahead of its barrier: S of tile k is issued after P V of tile k - 1 with
-    // NT = 2, but only after that of k - 2 with NT = 1, which therefore
-    // alternates between two barriers.
-    auto pv_done = [&](uint32_t k) {
-      return S::NT == 2 ? wait_warp(&sy.o_done[x], k & 1, sy, a) : wait_warp(&sy.o_done[k & 1], (k >> 1) & 1, sy, a);
-    };
+    auto pv_done = [&](uint32_t k) { return wait_warp(&sy.o_done[4 * x + (k & 3)], (k >> 2) & 1, sy, a); };
     Open open{0, 0, 0, 0, 0};                         // an item begun and not finished
     uint32_t merges = 0;
     for (; w.more() && ok; w.next()) {
@@ -862,12 +859,11 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       const int64_t clear = a.mask == DG_MASK_FULL ? w.keys() : a.mask == DG_MASK_CAUSAL ? (int64_t)w.past + i + 1 : w.past;
       float m = -INFINITY, l = 0.f;                   // m in log2 units
       for (int t = w.tb; t < w.te; ++t, ++gt) {
-        const int buf = S::NT == 2 ? x : (int)(gt & 1);
-        const uint32_t ph = S::NT == 2 ? gt & 1 : (gt >> 1) & 1;
-        if (!wait_warp(&sy.s_full[buf], ph, sy, a)) { ok = false; break; }
+        const int bar = 4 * x + (int)(gt & 3);
+        if (!wait_warp(&sy.s_full[bar], (gt >> 2) & 1, sy, a)) { ok = false; break; }
         if (any) {
           tc_fence_after();
-          const uint32_t t_s = tmem + buf * S::T_S + lanes;
+          const uint32_t t_s = tmem + (S::NT == 2 ? x : (int)(gt & 1)) * BN + lanes;
           const int64_t j0 = (int64_t)t * BN;
           const bool masked = __any_sync(0xffffffffu, j0 + BN > clear);
           // The usual tile, all columns seen: straight code, the next 16 columns on
@@ -990,7 +986,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sy.p_full[buf]);
+        if (lane == 0) mbar_arrive(&sy.p_full[bar]);
       }
       if (!ok) break;
       // ---------------------------------------------------------- the segment's result
@@ -1159,6 +1155,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     auto drain_queries = [&]() {
       if (q_landing) wait(&sy.q_full, q_phase, sy, a, false);
     };
+    // the slot of ring entry e is free: entry e - SL, a key tile's keys or values, has been taken
+    auto released = [&]() {
+      if (e < S::SL) return true;
+      const uint32_t k = (e - S::SL) >> 1, bar = 4 * (S::NT - 1) + (k & 3);
+      return wait_warp((e - S::SL) & 1 ? &sy.o_done[bar] : &sy.s_full[bar], (k >> 2) & 1, sy, a);
+    };
     auto position = [&]() { return (int64_t)(w.tb + (int)((e - e0) >> 1)) * BN; };
     auto to_clean = [&]() {                           // values that not every row of the item sees
       return ((e - e0) & 1) && a.mask != DG_MASK_FULL && position() + BN > w.clear();
@@ -1182,7 +1184,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           int eight, row[BN / 32];
           const bool boxes = find_eights<S>(w, pages, position(), &eight) && !clean;   // under the wait for the slot
           if (!boxes) find_rows<S>(w, position(), row);
-          if (!wait_warp(&sy.empty[part], ((e / S::SL) & 1) ^ 1, sy, a)) { ok = false; break; }
+          if (!released()) { ok = false; break; }
           landing = boxes;
           if (boxes) {                                // the copies arrive on `full` themselves
             copy_boxes<S>(a, kv ? &v_map : &k_map, eight, dst, &sy.full[part]);
@@ -1241,7 +1243,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
         for (; e - e0 < n; ++e) {
           const uint32_t at = e % S::AHEAD, slot = e % S::SL, dst = ring0 + slot * S::SLOT;
           if (!wait_warp(&sy.raw[at], (e / S::AHEAD) & 1, sy, a) ||
-              !wait_warp(&sy.empty[slot], ((e / S::SL) & 1) ^ 1, sy, a)) { ok = false; break; }
+              !released()) { ok = false; break; }
           convert<S>(sy.exps[at], r0, codes0 + at * S::RAW, dst);
           if (to_clean()) clean_rows<S, RW>(dst, r0, sy);
           fence_async_shared();
@@ -1262,82 +1264,61 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     // (the warp waits together, lane 0 issues)
     constexpr uint32_t id_s = idesc_bf16(128, BN, 0), id_o = idesc_bf16(128, S::DP, 1);
     const uint32_t q0 = smem_u32(smem), ring0 = smem_u32(ring);
-    uint32_t e = 0, gt = 0, seg = 0;                  // ring entries, key tiles and segments so far
+    uint32_t gt = 0, seg = 0;                         // key tiles and segments so far; tile k's keys and values
+                                                      // are ring entries 2 k and 2 k + 1
     bool ok = true;
     auto slot_full = [&](uint32_t entry) { return wait_warp(&sy.full[entry % S::SL], (entry / S::SL) & 1, sy, a); };
-    auto commit = [&](uint64_t* bar) { if (lane == 0) mma_commit(bar); };
-    auto scores = [&](uint32_t entry, int x, int buf) {   // S(buf) = Q(x) K^T
+    auto scores = [&](uint32_t k, int x, bool last) {   // S = Q(x) K^T of key tile k; the last of a segment frees Q
       tc_fence_after();
       if (lane == 0) {
-        const uint32_t k0 = ring0 + (entry % S::SL) * S::SLOT;
+        const uint32_t k0 = ring0 + (2 * k) % S::SL * S::SLOT;
 #pragma unroll
-        for (int k = 0; k < S::DP / 16; ++k)
-          mma_bf16(tmem + buf * S::T_S,
-                   sdesc(q0 + x * S::QTILE + (k >> 2) * (128 * 128) + (k & 3) * 32, 16, 1024),
-                   sdesc(k0 + (k >> 2) * (BN * 128) + (k & 3) * 32, 16, 1024), id_s, k ? 1u : 0u);
-        mma_commit(&sy.s_full[buf]);
+        for (int c = 0; c < S::DP / 16; ++c)
+          mma_bf16(tmem + (S::NT == 2 ? x : (int)(k & 1)) * BN,
+                   sdesc(q0 + x * S::QTILE + (c >> 2) * (128 * 128) + (c & 3) * 32, 16, 1024),
+                   sdesc(k0 + (c >> 2) * (BN * 128) + (c & 3) * 32, 16, 1024), id_s, c ? 1u : 0u);
+        mma_commit(&sy.s_full[4 * x + (k & 3)]);
+        if (last && x == S::NT - 1) mma_commit(&sy.q_free);
       }
     };
-    auto sums = [&](uint32_t entry, int x, int buf, bool first) {   // O(x) += P(buf) V
+    auto sums = [&](uint32_t k, int x, bool first) {    // O(x) += P V
       tc_fence_after();
       if (lane == 0) {
-        const uint32_t v0 = ring0 + (entry % S::SL) * S::SLOT;
+        const uint32_t v0 = ring0 + (2 * k + 1) % S::SL * S::SLOT;
 #pragma unroll
-        for (int k = 0; k < BN / 16; ++k)
-          mma_bf16_ts(tmem + S::T_O + x * S::DP, tmem + buf * S::T_S + k * 8,
-                      sdesc(v0 + k * 2048, BN * 128, 1024), id_o, first && k == 0 ? 0u : 1u);
-        mma_commit(&sy.o_done[S::NT == 2 ? x : buf]);
+        for (int c = 0; c < BN / 16; ++c)
+          mma_bf16_ts(tmem + S::T_O + x * S::DP, tmem + (S::NT == 2 ? x : (int)(k & 1)) * BN + c * 8,
+                      sdesc(v0 + c * 2048, BN * 128, 1024), id_o, first && c == 0 ? 0u : 1u);
+        mma_commit(&sy.o_done[4 * x + (k & 3)]);
       }
     };
     for (; w.more() && ok; w.next(), ++seg) {
-      if (!wait_warp(&sy.q_full, seg & 1, sy, a) || !slot_full(e)) { ok = false; break; }
+      if (!wait_warp(&sy.q_full, seg & 1, sy, a) || !slot_full(2 * gt)) { ok = false; break; }
       const int n = w.te - w.tb;
-      if constexpr (S::NT == 2) {
-        scores(e, 0, 0);
-        scores(e, 1, 1);
-        commit(&sy.empty[e % S::SL]);
-        if (n == 1) commit(&sy.q_free);
-        for (int t = 0; t < n && ok; ++t, ++gt, e += 2) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!wait_warp(&sy.p_full[x], gt & 1, sy, a) ||
-                (t == 0 && seg && !wait_warp(&sy.o_free[x], (seg - 1) & 1, sy, a)) ||
-                (x == 0 && !slot_full(e + 1))) { ok = false; break; }
-            sums(e + 1, x, x, t == 0);
-            if (x == 1) commit(&sy.empty[(e + 1) % S::SL]);
-            if (t + 1 < n) {
-              if (x == 0 && !slot_full(e + 2)) { ok = false; break; }
-              scores(e + 2, x, x);
-              if (x == 1) {
-                commit(&sy.empty[(e + 2) % S::SL]);
-                if (t + 2 == n) commit(&sy.q_free);
-              }
-            }
-          }
+      for (int x = 0; x < S::NT; ++x) scores(gt, x, n == 1);
+      for (int t = 0; t < n && ok; ++t, ++gt) {
+        if (S::NT == 1 && t + 1 < n) {                  // the next S has a buffer of its own
+          if (!slot_full(2 * gt + 2)) { ok = false; break; }
+          scores(gt + 1, 0, t + 2 == n);
         }
-      } else {
-        scores(e, 0, gt & 1);
-        commit(&sy.empty[e % S::SL]);
-        if (n == 1) commit(&sy.q_free);
-        for (int t = 0; t < n && ok; ++t, ++gt, e += 2) {
-          if (t + 1 < n) {
-            if (!slot_full(e + 2)) { ok = false; break; }
-            scores(e + 2, 0, (gt + 1) & 1);
-            commit(&sy.empty[(e + 2) % S::SL]);
-            if (t + 2 == n) commit(&sy.q_free);
-          }
-          if (!wait_warp(&sy.p_full[gt & 1], (gt >> 1) & 1, sy, a) ||
-              (t == 0 && seg && !wait_warp(&sy.o_free[0], (seg - 1) & 1, sy, a)) || !slot_full(e + 1)) {
+#pragma unroll
+        for (int x = 0; x < S::NT; ++x) {
+          if (!wait_warp(&sy.p_full[4 * x + (gt & 3)], (gt >> 2) & 1, sy, a) ||
+              (t == 0 && seg && !wait_warp(&sy.o_free[x], (seg - 1) & 1, sy, a)) || (x == 0 && !slot_full(2 * gt + 1))) {
             ok = false;
             break;
           }
-          sums(e + 1, 0, gt & 1, t == 0);
-          commit(&sy.empty[(e + 1) % S::SL]);
+          sums(gt, x, t == 0);
+          if (S::NT == 2 && t + 1 < n) {
+            if (x == 0 && !slot_full(2 * gt + 2)) { ok = false; break; }
+            scores(gt + 1, x, t + 2 == n);
+          }
         }
       }
     }
     // every MMA issued has completed before TMEM is released and the CTA exits
-    commit(&sy.fin);
+    if (lane == 0) mma_commit(&sy.fin);
     wait(&sy.fin, 0, sy, a, false);
     __syncwarp();
   }
