@@ -329,6 +329,15 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Sync& 
   return __all_sync(0xffffffffu, wait(bar, parity, sy, a)) != 0;
 }
 
+// A value that is the same in every lane, made visibly so.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // D (TMEM) += A (TMEM, bf16) B (shared memory).
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -1268,29 +1277,41 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
                                                       // are ring entries 2 k and 2 k + 1
     bool ok = true;
     auto slot_full = [&](uint32_t entry) { return wait_warp(&sy.full[entry % S::SL], (entry / S::SL) & 1, sy, a); };
+    // Addresses and descriptors are made the same in every lane, in a form the
+    // compiler can see (uniform registers are what the MMA takes), once for each
+    // product, and one elected lane issues: building them in a divergent lane for
+    // each instruction cost more than the MMA's own time.
+    const uint32_t tm = uniform(tmem);
+    const uint64_t qd = sdesc(uniform(q0), 16, 1024);
+    const uint64_t kd = sdesc(uniform(ring0), 16, 1024), vd = sdesc(uniform(ring0), BN * 128, 1024);
     auto scores = [&](uint32_t k, int x, bool last) {   // S = Q(x) K^T of key tile k; the last of a segment frees Q
       tc_fence_after();
-      if (lane == 0) {
-        const uint32_t k0 = ring0 + (2 * k) % S::SL * S::SLOT;
+      const uint64_t b = kd + uniform((2 * k) % S::SL) * (uint64_t)(S::SLOT / 16);
+      const uint32_t d = tm + uniform(S::NT == 2 ? x : (int)(k & 1)) * BN;
+      uint64_t* bar = &sy.s_full[uniform(4 * x + (k & 3))];
+      if (elected()) {
 #pragma unroll
         for (int c = 0; c < S::DP / 16; ++c)
-          mma_bf16(tmem + (S::NT == 2 ? x : (int)(k & 1)) * BN,
-                   sdesc(q0 + x * S::QTILE + (c >> 2) * (128 * 128) + (c & 3) * 32, 16, 1024),
-                   sdesc(k0 + (c >> 2) * (BN * 128) + (c & 3) * 32, 16, 1024), id_s, c ? 1u : 0u);
-        mma_commit(&sy.s_full[4 * x + (k & 3)]);
+          mma_bf16(d, qd + (x * S::QTILE + (c >> 2) * (128 * 128) + (c & 3) * 32) / 16,
+                   b + ((c >> 2) * (BN * 128) + (c & 3) * 32) / 16, id_s, c ? 1u : 0u);
+        mma_commit(bar);
         if (last && x == S::NT - 1) mma_commit(&sy.q_free);
       }
+      __syncwarp();
     };
     auto sums = [&](uint32_t k, int x, bool first) {    // O(x) += P V
       tc_fence_after();
-      if (lane == 0) {
-        const uint32_t v0 = ring0 + (2 * k + 1) % S::SL * S::SLOT;
+      const uint64_t b = vd + uniform((2 * k + 1) % S::SL) * (uint64_t)(S::SLOT / 16);
+      const uint32_t p = tm + uniform(S::NT == 2 ? x : (int)(k & 1)) * BN;
+      uint64_t* bar = &sy.o_done[uniform(4 * x + (k & 3))];
+      const uint32_t add = uniform(first ? 0u : 1u);
+      if (elected()) {
 #pragma unroll
         for (int c = 0; c < BN / 16; ++c)
-          mma_bf16_ts(tmem + S::T_O + x * S::DP, tmem + (S::NT == 2 ? x : (int)(k & 1)) * BN + c * 8,
-                      sdesc(v0 + c * 2048, BN * 128, 1024), id_o, first && c == 0 ? 0u : 1u);
-        mma_commit(&sy.o_done[4 * x + (k & 3)]);
+          mma_bf16_ts(tm + S::T_O + x * S::DP, p + c * 8, b + c * (2048 / 16), id_o, c ? 1u : add);
+        mma_commit(bar);
       }
+      __syncwarp();
     };
     for (; w.more() && ok; w.next(), ++seg) {
       if (!wait_warp(&sy.q_full, seg & 1, sy, a) || !slot_full(2 * gt)) { ok = false; break; }
@@ -1318,7 +1339,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       }
     }
     // every MMA issued has completed before TMEM is released and the CTA exits
-    if (lane == 0) mma_commit(&sy.fin);
+    if (elected()) mma_commit(&sy.fin);
+    __syncwarp();
     wait(&sy.fin, 0, sy, a, false);
     __syncwarp();
   }
