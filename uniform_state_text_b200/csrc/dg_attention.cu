@@ -107,7 +107,7 @@ struct Shape {
   static constexpr int BN = DP == 256 ? 64 : 128;      // keys per tile
   static constexpr int SLOT = BN * DP * 2;
   static constexpr int QTILE = 128 * DP * 2;
-  static constexpr int SL = F8 ? (DP == 64 ? 6 : 4) : DP == 256 ? 4 : DP == 128 ? (NT == 2 ? 4 : 5) : (NT == 2 ? 6 : 8);   // ring slots
+  static constexpr int SL = F8 ? (DP == 64 ? 6 : 4) : DP == 256 ? 4 : DP == 128 ? 5 : (NT == 2 ? 6 : 8);   // ring slots
   // Load warps. bf16: one per slot. e4m3: CW that convert each tile together, so
   // that a slot is not held longer than its share of the time, and one that
   // brings the codes AHEAD tiles before.
@@ -292,7 +292,8 @@ struct Sync {
   uint64_t s_full[8], p_full[8];   // 4 x + k mod 4: S ready (the keys' slot is free after the last x), P stored
   uint64_t o_done[8], o_free[2];   // P V done (the values' slot is free after the last x); O read
   uint64_t q_full, q_free, fin;
-  uint64_t raw[4], taken[4];       // e4m3: a tile's codes have landed, and have been converted
+  uint64_t raw[8], taken[4];       // e4m3: a tile's codes have landed, and have been converted (bf16: a value
+                                   // tile to be cleaned has landed)
   uint8_t exps[4][128];            // their rows' exponents
   uint64_t merge;                  // between the four warps that share a tile's rows
   uint32_t tmem;
@@ -546,15 +547,17 @@ struct Pages {
   int b = -1, base = 0, page = 0;
 };
 // The same for TMA, by eights (a.box != 0: page_size is a multiple of 8): lane l
-// gets the cache row of position j0 + 8 l, l < BN / 8; whether all rows of the
-// tile are there.
+// gets the cache row of position j0 + 8 l, l < BN / 8 (behind the sequence's end
+// any row: the keys there are masked, the values set to zero); whether all rows
+// up to the end have pages.
 template <class S, typename W>
 __device__ __forceinline__ bool find_eights(const W& w, Pages& pg, int64_t j0, int* eight) {
   *eight = -1;
-  if (w.a.box == 0 || j0 + S::BN > w.keys()) return false;
+  if (w.a.box == 0 || j0 >= w.keys()) return false;
   const dg_kv_cache& c = w.a.w.c;
   const int lane = threadIdx.x & 31;
-  const uint32_t ps = (uint32_t)c.page_size, lo = (uint32_t)j0 / ps, j = (uint32_t)j0 + lane * 8, at = j / ps;
+  const uint32_t ps = (uint32_t)c.page_size, lo = (uint32_t)j0 / ps;
+  const uint32_t j = (int64_t)j0 + lane * 8 < w.keys() ? (uint32_t)j0 + lane * 8 : (uint32_t)j0, at = j / ps;
   if (pg.b != w.b || (int)lo < pg.base || (int)(((uint32_t)j0 + S::BN - 8) / ps) >= pg.base + 32) {
     pg.b = w.b;
     pg.base = (int)lo;
@@ -618,7 +621,7 @@ __device__ __forceinline__ void copy_boxes(const Args& a, const CUtensorMap* map
   constexpr int NB = S::DP / 64;
   const int lane = threadIdx.x & 31;
   const int run = lane / NB * a.box, cb = lane % NB;            // the lane's rows and 64-column block
-  const int first = __shfl_sync(0xffffffffu, eight, (run >> 3) & 31);
+  const int first = __shfl_sync(0xffffffffu, eight, (run >> 3) & 31);   // (a run lies in one page, its head before the end)
   if (lane == 0) mbar_expect_tx(bar, S::BN * S::DP * (S::F8 ? 1 : 2));
   __syncwarp();
   if (run < S::BN)
@@ -711,22 +714,31 @@ __device__ __forceinline__ void convert(const uint8_t* exps, int r0, uint32_t sr
   }
 }
 
-// What is not finite in rows r0 to r0 + RW of a slot replaced by zero and noted. For
-// value tiles that hold positions which a query row of the item may not see:
-// 0 x NaN in the second product would reach every row.
+// Rows r0 to r0 + RW of a value tile in its slot: those from `live` on, behind
+// the sequence's end, become zeros; with `scrub`, what is not finite in the
+// others too, and is noted. For tiles that hold positions which a query row of
+// the item may not see: 0 x NaN in the second product would reach every row.
 template <class S, int RW>
-__device__ __forceinline__ void clean_rows(uint32_t slot, int r0, Sync& sy) {
-  constexpr int CPR = S::DP / 8, RPI = 32 / CPR;
+__device__ __forceinline__ void clean_rows(uint32_t slot, int r0, int live, bool scrub, Sync& sy) {
+  constexpr int CPR = S::DP / 8, RPI = 32 / CPR, N = RW / RPI;
   const int lane = threadIdx.x & 31, c = lane % CPR;
   bool dirty = false;
   __syncwarp();
-  for (int it = 0; it < RW / RPI; ++it) {
-    const uint32_t at = slot + swizzled(r0 + it * RPI + lane / CPR, c, S::BN);
-    const uint4 v = ld_shared(at);
-    const uint4 f = make_uint4(only_finite(v.x), only_finite(v.y), only_finite(v.z), only_finite(v.w));
-    if (f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w) {
-      st_shared(at, f);
-      dirty = true;
+#pragma unroll 4
+  for (int it = 0; it < N; ++it) {
+    const int r = r0 + it * RPI + lane / CPR;
+    const uint32_t at = slot + swizzled(r, c, S::BN);
+    if (r >= live) {
+      st_shared(at, make_uint4(0, 0, 0, 0));
+    } else if (scrub) {
+      const uint4 v = ld_shared(at);
+      // an exponent of all ones carries into the sign's place
+      const uint32_t t = ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
+                         ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
+      if (t & 0x80008000u) {
+        st_shared(at, make_uint4(only_finite(v.x), only_finite(v.y), only_finite(v.z), only_finite(v.w)));
+        dirty = true;
+      }
     }
   }
   if (dirty) *(volatile int*)&sy.nonfinite = 1;
@@ -824,7 +836,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     mbar_init(&sy.q_free, 1);
     mbar_init(&sy.fin, 1);
     mbar_init(&sy.merge, 4);
-    for (int x = 0; x < S::AHEAD; ++x) { mbar_init(&sy.raw[x], 33); mbar_init(&sy.taken[x], S::CW); }
+    for (int x = 0; x < 8; ++x) mbar_init(&sy.raw[x], S::F8 ? 33 : 1);
+    for (int x = 0; x < S::AHEAD; ++x) mbar_init(&sy.taken[x], S::CW);
     sy.abort = 0;
     sy.nonfinite = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -955,7 +968,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
                 const uint64_t x = fma2(pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), sc, ns);
-                const uint64_t e = (j & 3) == 3 ? exp2_poly2(x) : exp2_mufu2(x);
+                const uint64_t e = S::NT == 2 && (j & 3) == 3 ? exp2_poly2(x) : exp2_mufu2(x);
                 ls = add2(ls, e);
                 p[j] = pack_bf16(lo2(e), hi2(e));
               }
@@ -1171,12 +1184,13 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       return wait_warp((e - S::SL) & 1 ? &sy.o_done[bar] : &sy.s_full[bar], (k >> 2) & 1, sy, a);
     };
     auto position = [&]() { return (int64_t)(w.tb + (int)((e - e0) >> 1)) * BN; };
-    auto to_clean = [&]() {                           // values that not every row of the item sees
-      return ((e - e0) & 1) && a.mask != DG_MASK_FULL && position() + BN > w.clear();
-    };
+    // of entry e: its rows before the sequence's end; whether it holds values that not every row of the item sees
+    auto live_rows = [&]() { return (int)min((int64_t)BN, w.keys() - position()); };
+    auto to_scrub = [&]() { return ((e - e0) & 1) && a.mask != DG_MASK_FULL && position() + BN > w.clear(); };
     if constexpr (!S::F8) {
       // one warp per slot, entries SL apart
       bool landing = false;                           // the slot's last copy is by TMA, and has not been waited for
+      uint32_t raws = 0;
       e = part;
       for (; w.more() && ok; w.next(), ++seg) {
         const uint32_t n = 2 * (uint32_t)(w.te - w.tb);
@@ -1188,20 +1202,31 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
             if (!queries()) { ok = false; break; }
           }
           if (e - e0 >= n) break;
-          const bool kv = (e - e0) & 1, clean = to_clean();
+          const bool kv = (e - e0) & 1, scrub = to_scrub();
+          const int live = live_rows();
+          const bool clean = scrub || (kv && live < BN);
           const uint32_t dst = ring0 + part * S::SLOT;
           int eight, row[BN / 32];
-          const bool boxes = find_eights<S>(w, pages, position(), &eight) && !clean;   // under the wait for the slot
+          const bool boxes = find_eights<S>(w, pages, position(), &eight);    // under the wait for the slot
           if (!boxes) find_rows<S>(w, position(), row);
           if (!released()) { ok = false; break; }
-          landing = boxes;
-          if (boxes) {                                // the copies arrive on `full` themselves
+          landing = boxes && !clean;
+          if (landing) {                              // the copies arrive on `full` themselves
             copy_boxes<S>(a, kv ? &v_map : &k_map, eight, dst, &sy.full[part]);
             continue;
           }
-          copy_rows<S>(a, kv ? a.w.c.v : a.w.c.k, row, dst);
-          copies_landed();
-          if (clean) clean_rows<S, BN>(dst, 0, sy);
+          if (boxes) {
+            copy_boxes<S>(a, &v_map, eight, dst, &sy.raw[part]);
+            if (!wait_warp(&sy.raw[part], raws++ & 1, sy, a)) {
+              wait(&sy.raw[part], (raws - 1) & 1, sy, a, false);
+              ok = false;
+              break;
+            }
+          } else {
+            copy_rows<S>(a, kv ? a.w.c.v : a.w.c.k, row, dst);
+            copies_landed();
+          }
+          if (clean) clean_rows<S, BN>(dst, 0, live, scrub, sy);
           fence_async_shared();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sy.full[part]);
@@ -1254,7 +1279,9 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           if (!wait_warp(&sy.raw[at], (e / S::AHEAD) & 1, sy, a) ||
               !released()) { ok = false; break; }
           convert<S>(sy.exps[at], r0, codes0 + at * S::RAW, dst);
-          if (to_clean()) clean_rows<S, RW>(dst, r0, sy);
+          const bool scrub = to_scrub();
+          const int live = live_rows();
+          if (scrub || (((e - e0) & 1) && live < r0 + RW)) clean_rows<S, RW>(dst, r0, live, scrub, sy);
           fence_async_shared();
           __syncwarp();
           if (lane == 0) {
