@@ -72,8 +72,10 @@ struct Args {
   const __nv_bfloat16* q;
   int64_t q_ts, q_hs;
   int q_heads, G;              // G query heads per key/value head
-  uint32_t g_mul;              // r / G = r g_mul >> g_shift, exact for r < 2^31
-  int g_shift;
+  // r / G and position / page_size as products, exact below 2^31 (a division for
+  // every tile and row had cost more than the tile's copies)
+  uint32_t g_mul, ps_mul;
+  int g_shift, ps_shift;
   float scale_log2;            // scale log2(e)
   int mask;
   const uint32_t* tree;
@@ -90,6 +92,9 @@ struct Args {
 
   __device__ __forceinline__ uint32_t over_g(uint32_t r) const {
     return (uint32_t)(((uint64_t)r * g_mul) >> g_shift);
+  }
+  __device__ __forceinline__ uint32_t over_page(uint32_t pos) const {
+    return (uint32_t)(((uint64_t)pos * ps_mul) >> ps_shift);
   }
 };
 
@@ -499,34 +504,19 @@ __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t pair, float scale) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
   return pack_bf16(f.x * scale, f.y * scale);
 }
-// 16 codes, by their bits: the code's exponent and mantissa moved to where bf16
-// has them make code x 2^-120 (its subnormals bf16's own), and one product with
-// 2^(120 + e) makes the value; 52 integer and 8 packed instructions against 48
-// conversions, of which the hardware does a quarter as many per cycle. `pow`
-// is 2^(120 + e) twice, for e <= 7; beyond that, and where a code is NaN, the
-// conversions are taken.
-__device__ __forceinline__ void codes16_to_bf16(const uint4& v, uint32_t pow, float scale, bool large, uint32_t* o) {
-  const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-  uint32_t nan = 0;
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    nan |= (x[t] & 0x7f7f7f7fu) + 0x01010101u;
-    const uint32_t hi = (x[t] & 0x80808080u) | ((x[t] >> 4) & 0x07070707u);
-    const uint32_t lo = (x[t] << 4) & 0xf0f0f0f0u;
-    const uint32_t a = __byte_perm(lo, hi, 0x5140), b = __byte_perm(lo, hi, 0x7362);
-    const __nv_bfloat162 p = *reinterpret_cast<const __nv_bfloat162*>(&pow);
-    const __nv_bfloat162 c = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), p);
-    const __nv_bfloat162 d = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), p);
-    o[2 * t] = *reinterpret_cast<const uint32_t*>(&c);
-    o[2 * t + 1] = *reinterpret_cast<const uint32_t*>(&d);
-  }
-  if (large || (nan & 0x80808080u)) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      o[2 * t] = codes_to_bf16(x[t], scale);
-      o[2 * t + 1] = codes_to_bf16(x[t] >> 16, scale);
+// kv_row() with the division as a product.
+__device__ __forceinline__ int cache_row(const Args& a, const int32_t* table, int64_t pos, int head) {
+  const dg_kv_cache& c = a.w.c;
+  if (pos >= 0 && pos <= 0x7fffffff) {
+    const uint32_t at = a.over_page((uint32_t)pos);
+    if (at < (uint32_t)a.w.b.table_stride) {
+      const int page = __ldg(table + at);
+      if (page >= 0 && page < c.pages)
+        return (page * c.kv_heads + head) * c.page_size + (int)((uint32_t)pos - at * (uint32_t)c.page_size);
     }
   }
+  raise_status(c.status, DG_EINVAL);
+  return -1;
 }
 
 // The cache rows of a key tile: rows lane, lane + 32, ... from position j0 on; -1
@@ -538,7 +528,7 @@ __device__ __forceinline__ void find_rows(const W& w, int64_t j0, int* row) {
 #pragma unroll
   for (int p = 0; p < S::BN / 32; ++p) {
     const int64_t j = j0 + p * 32 + (threadIdx.x & 31);
-    row[p] = j < L ? kv_row(w.a.w, table, j, w.h) : -1;
+    row[p] = j < L ? cache_row(w.a, table, j, w.h) : -1;
   }
 }
 // 32 entries of a sequence's page table in the lanes of a warp: a look-up per tile
@@ -556,9 +546,9 @@ __device__ __forceinline__ bool find_eights(const W& w, Pages& pg, int64_t j0, i
   if (w.a.box == 0 || j0 >= w.keys()) return false;
   const dg_kv_cache& c = w.a.w.c;
   const int lane = threadIdx.x & 31;
-  const uint32_t ps = (uint32_t)c.page_size, lo = (uint32_t)j0 / ps;
-  const uint32_t j = (int64_t)j0 + lane * 8 < w.keys() ? (uint32_t)j0 + lane * 8 : (uint32_t)j0, at = j / ps;
-  if (pg.b != w.b || (int)lo < pg.base || (int)(((uint32_t)j0 + S::BN - 8) / ps) >= pg.base + 32) {
+  const uint32_t ps = (uint32_t)c.page_size, lo = w.a.over_page((uint32_t)j0);
+  const uint32_t j = (int64_t)j0 + lane * 8 < w.keys() ? (uint32_t)j0 + lane * 8 : (uint32_t)j0, at = w.a.over_page(j);
+  if (pg.b != w.b || (int)lo < pg.base || (int)w.a.over_page((uint32_t)j0 + S::BN - 8) >= pg.base + 32) {
     pg.b = w.b;
     pg.base = (int)lo;
     const int64_t t = (int64_t)lo + lane;
@@ -677,40 +667,35 @@ __device__ __forceinline__ void query_boxes(const W& w, const CUtensorMap* map, 
   __syncwarp();
 }
 
-// e4m3: rows r0 to r0 + BN / CW of a tile of codes to bf16 in a ring slot.
+// e4m3: rows r0 to r0 + BN / CW of a tile of codes to bf16 in a ring slot. (The
+// same by moving the codes' bits and one packed product took as long: 48
+// conversions and products or 60 integer instructions for 16 codes.)
 template <class S>
 __device__ __forceinline__ void convert(const uint8_t* exps, int r0, uint32_t src, uint32_t slot) {
   constexpr int RW = S::BN / S::CW, K = RW / 8, NB = S::DP / 64;
   const int lane = threadIdx.x & 31, q = lane & 3, rl = lane >> 2;
-  uint32_t e[K], large = 0;
+  float scale[K];                                    // any byte is an exponent, also in rows never written
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    // any byte is an exponent, also in rows never written
-    e[k] = max(1u, min(254u, (uint32_t)exps[r0 + k * 8 + rl]));
-    large |= e[k] > 134;
-  }
-  const bool conversions = __any_sync(0xffffffffu, large);
-  uint4 v[K];
-  auto load = [&](int cb) {
-    const uint32_t at = src + (cb * S::BN + r0) * 64 + lane * 16;
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = ld_shared(at + k * 512);
-  };
+  for (int k = 0; k < K; ++k) scale[k] = __uint_as_float(max(1u, min(254u, (uint32_t)exps[r0 + k * 8 + rl])) << 23);
   const uint32_t c0 = ((2 * q) ^ rl) << 4, c1 = ((2 * q + 1) ^ rl) << 4;
-  // The loop stays a loop: unrolled, its code streamed through the instruction
-  // cache and took four times as long.
-  load(0);
-#pragma unroll 1
+#pragma unroll
   for (int cb = 0; cb < NB; ++cb) {
-    const uint32_t to = slot + cb * (S::BN * 128) + (r0 + rl) * 128;
+    const uint32_t from = src + (cb * S::BN + r0) * 64 + lane * 16, to = slot + cb * (S::BN * 128) + (r0 + rl) * 128;
+    uint4 v[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = ld_shared(from + k * 512);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+      const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
       uint32_t o[8];
-      codes16_to_bf16(v[k], min(e[k] + 120, 254u) * 0x00800080u, __uint_as_float(e[k] << 23), conversions, o);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        o[2 * t] = codes_to_bf16(x[t], scale[k]);
+        o[2 * t + 1] = codes_to_bf16(x[t] >> 16, scale[k]);
+      }
       st_shared(to + k * 1024 + c0, make_uint4(o[0], o[1], o[2], o[3]));
       st_shared(to + k * 1024 + c1, make_uint4(o[4], o[5], o[6], o[7]));
     }
-    if (cb + 1 < NB) load(cb + 1);
   }
 }
 
@@ -756,7 +741,7 @@ __device__ __noinline__ float4 with_not_finite(const W w, const uint32_t* tree, 
   const int64_t end = min(w.keys(), (int64_t)w.te * S::BN);
   for (int64_t j = max(from, (int64_t)w.tb * S::BN); j < end; ++j) {
     if (!(seen(w, tree, i, j) & 1)) continue;
-    const int row = kv_row(a.w, a.w.b.page_table + (int64_t)w.b * a.w.b.table_stride, j, w.h);
+    const int row = cache_row(a, a.w.b.page_table + (int64_t)w.b * a.w.b.table_stride, j, w.h);
     if (row < 0) continue;
     const int64_t at = (int64_t)row * a.w.c.head_dim + d;
     if constexpr (S::F8) {
@@ -836,7 +821,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     mbar_init(&sy.q_free, 1);
     mbar_init(&sy.fin, 1);
     mbar_init(&sy.merge, 4);
-    for (int x = 0; x < 8; ++x) mbar_init(&sy.raw[x], S::F8 ? 33 : 1);
+    for (int x = 0; x < 8; ++x) mbar_init(&sy.raw[x], S::F8 ? 1 + BN / 8 : 1);
     for (int x = 0; x < S::AHEAD; ++x) mbar_init(&sy.taken[x], S::CW);
     sy.abort = 0;
     sy.nonfinite = 0;
@@ -1249,19 +1234,21 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           if (!wait_warp(&sy.taken[at], ((e / S::AHEAD) & 1) ^ 1, sy, a)) { ok = false; break; }
           if (boxes) {
             copy_boxes<S>(a, kv ? &v_map : &k_map, eight, dst, &sy.raw[at]);
-            if (eight >= 0)
-              asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(&sy.exps[at][lane * 8])), "l"(exps + eight)
+            // an arrival of each of these lanes when its eight exponents have landed
+            if (lane < BN / 8)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n\t"
+                           "cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%2];" ::"r"(smem_u32(&sy.exps[at][lane * 8])),
+                           "l"(exps + eight), "r"(smem_u32(&sy.raw[at]))
                            : "memory");
           } else {
             copy_rows<S>(a, kv ? a.w.c.v : a.w.c.k, row, dst);
 #pragma unroll
             for (int p = 0; p < BN / 32; ++p)
               sy.exps[at][p * 32 + lane] = row[p] >= 0 ? __ldg(exps + row[p]) : (uint8_t)127;
+            copies_landed();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sy.raw[at]);
+            if (lane <= BN / 8) mbar_arrive(&sy.raw[at]);
           }
-          // one arrival of each lane when its own copies have landed
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sy.raw[at])) : "memory");
         }
         e0 += n;
       }
@@ -1610,12 +1597,12 @@ extern "C" int dg_cache_attention(const dg_kv_cache* cache, const dg_kv_batch* b
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return kv_launched(e);
   char* sc = static_cast<char*>(scratch);
-  const uint32_t G = (uint32_t)(q_heads / cache->kv_heads);
-  int log = 0;                                     // r / G for r < 2^31: 2^log >= G, the multiplier rounded up
-  while ((1ll << log) < G) ++log;
-  const uint32_t mul = (uint32_t)(((1ull << (31 + log)) + G - 1) / G);
+  const uint32_t G = (uint32_t)(q_heads / cache->kv_heads), ps = (uint32_t)cache->page_size;
+  // r / n for r < 2^31: 2^log >= n, the multiplier rounded up
+  auto log_of = [](uint32_t n) { int log = 0; while ((1ull << log) < n) ++log; return log; };
+  auto mul_of = [&](uint32_t n) { return (uint32_t)(((1ull << (31 + log_of(n))) + n - 1) / n); };
   const Args a{{*cache, *batch}, static_cast<const __nv_bfloat16*>(q), q_ts, q_hs, q_heads,
-               (int)G, mul, 31 + log, scale * 1.4426950408889634f, mask, tree_mask, mask_words,
+               (int)G, mul_of(G), mul_of(ps), 31 + log_of(G), 31 + log_of(ps), scale * 1.4426950408889634f, mask, tree_mask, mask_words,
                static_cast<__nv_bfloat16*>(out), lse, reinterpret_cast<float*>(sc + p.o),
                reinterpret_cast<float2*>(sc + p.ml), reinterpret_cast<Open*>(sc + p.open), p.rows, 0, 0};
   const int ctas = std::min(sms, kMaxCtas);
