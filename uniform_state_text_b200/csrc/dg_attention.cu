@@ -113,10 +113,11 @@ struct Shape {
   static constexpr int SLOT = BN * DP * 2;
   static constexpr int QTILE = 128 * DP * 2;
   static constexpr int SL = F8 ? (DP == 64 ? 6 : 4) : DP == 256 ? 4 : DP == 128 ? 5 : (NT == 2 ? 6 : 8);   // ring slots
-  // Load warps. bf16: one per slot. e4m3: CW that convert each tile together, so
+  // Load warps. bf16: one per slot. e4m3: CW that convert, several to a tile, so
   // that a slot is not held longer than its share of the time, and one that
   // brings the codes AHEAD tiles before.
   static constexpr int CW = F8 ? (NT == 1 ? 8 : 4) : 0;
+  static constexpr int TEAM = F8 ? CW / 2 : 1;         // half convert keys, half values
   static constexpr int N_LOAD = F8 ? CW : SL;
   static constexpr int AHEAD = F8 ? (DP == 64 ? 4 : DP == 128 && NT == 1 ? 3 : 2) : 0;
   static constexpr int RAW = BN * DP;                  // bytes of a tile's codes
@@ -667,17 +668,19 @@ __device__ __forceinline__ void query_boxes(const W& w, const CUtensorMap* map, 
   __syncwarp();
 }
 
-// e4m3: rows r0 to r0 + BN / CW of a tile of codes to bf16 in a ring slot. (The
+// e4m3: rows r0 to r0 + BN / TEAM of a tile of codes to bf16 in a ring slot. (The
 // same by moving the codes' bits and one packed product took as long: 48
 // conversions and products or 60 integer instructions for 16 codes.)
 template <class S>
 __device__ __forceinline__ void convert(const uint8_t* exps, int r0, uint32_t src, uint32_t slot) {
-  constexpr int RW = S::BN / S::CW, K = RW / 8, NB = S::DP / 64;
+  constexpr int RW = S::BN / S::TEAM, K = RW < 32 ? RW / 8 : 4, NB = S::DP / 64;
   const int lane = threadIdx.x & 31, q = lane & 3, rl = lane >> 2;
+  const uint32_t c0 = ((2 * q) ^ rl) << 4, c1 = ((2 * q + 1) ^ rl) << 4;
+#pragma unroll 1
+  for (int end = r0 + RW; r0 < end; r0 += 8 * K) {
   float scale[K];                                    // any byte is an exponent, also in rows never written
 #pragma unroll
   for (int k = 0; k < K; ++k) scale[k] = __uint_as_float(max(1u, min(254u, (uint32_t)exps[r0 + k * 8 + rl])) << 23);
-  const uint32_t c0 = ((2 * q) ^ rl) << 4, c1 = ((2 * q + 1) ^ rl) << 4;
 #pragma unroll
   for (int cb = 0; cb < NB; ++cb) {
     const uint32_t from = src + (cb * S::BN + r0) * 64 + lane * 16, to = slot + cb * (S::BN * 128) + (r0 + rl) * 128;
@@ -696,6 +699,7 @@ __device__ __forceinline__ void convert(const uint8_t* exps, int r0, uint32_t sr
       st_shared(to + k * 1024 + c0, make_uint4(o[0], o[1], o[2], o[3]));
       st_shared(to + k * 1024 + c1, make_uint4(o[4], o[5], o[6], o[7]));
     }
+  }
   }
 }
 
@@ -810,7 +814,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S::SL; ++s) mbar_init(&sy.full[s], S::F8 ? S::CW : 1);
+    for (int s = 0; s < S::SL; ++s) mbar_init(&sy.full[s], S::F8 ? S::TEAM : 1);
     for (int x = 0; x < 8; ++x) {
       mbar_init(&sy.s_full[x], 1);
       mbar_init(&sy.p_full[x], 4);
@@ -822,7 +826,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     mbar_init(&sy.fin, 1);
     mbar_init(&sy.merge, 4);
     for (int x = 0; x < 8; ++x) mbar_init(&sy.raw[x], S::F8 ? 1 + BN / 8 : 1);
-    for (int x = 0; x < S::AHEAD; ++x) mbar_init(&sy.taken[x], S::CW);
+    for (int x = 0; x < S::AHEAD; ++x) mbar_init(&sy.taken[x], S::TEAM);
     sy.abort = 0;
     sy.nonfinite = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1256,12 +1260,13 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       for (uint32_t x = e > S::AHEAD ? e - S::AHEAD : 0; x < e; ++x)
         wait(&sy.raw[x % S::AHEAD], (x / S::AHEAD) & 1, sy, a, false);
     } else {
-      // all warps together on every entry, each its own rows
-      constexpr int RW = BN / S::CW;
-      const int r0 = part * RW;
+      // half of the warps on the keys, half on the values, each its own rows
+      constexpr int RW = BN / S::TEAM;
+      const uint32_t team = part / S::TEAM;
+      const int r0 = part % S::TEAM * RW;
       for (; w.more() && ok; w.next(), ++seg) {
         const uint32_t n = 2 * (uint32_t)(w.te - w.tb);
-        for (; e - e0 < n; ++e) {
+        for (e = e0 + team; e - e0 < n; e += 2) {
           const uint32_t at = e % S::AHEAD, slot = e % S::SL, dst = ring0 + slot * S::SLOT;
           if (!wait_warp(&sy.raw[at], (e / S::AHEAD) & 1, sy, a) ||
               !released()) { ok = false; break; }
@@ -1276,7 +1281,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
             mbar_arrive(&sy.taken[at]);
           }
           // the queries, once the first entry is on its way
-          if (e == e0 && !queries()) { ok = false; break; }
+          if (e - e0 < 2 && !queries()) { ok = false; break; }
         }
         e0 += n;
       }
