@@ -112,18 +112,19 @@ struct Shape {
   static constexpr int BN = DP == 256 ? 64 : 128;      // keys per tile
   static constexpr int SLOT = BN * DP * 2;
   static constexpr int QTILE = 128 * DP * 2;
-  static constexpr int SL = F8 ? (DP == 64 ? 6 : 4) : DP == 256 ? 4 : DP == 128 ? 5 : (NT == 2 ? 6 : 8);   // ring slots
+  static constexpr int SL = F8 ? (DP == 64 ? 6 : DP == 128 && NT == 1 ? 3 : 4) : DP == 256 ? 4 : DP == 128 ? 5 : (NT == 2 ? 6 : 8);   // ring slots
   // Load warps. bf16: one per slot. e4m3: CW that convert, several to a tile, so
-  // that a slot is not held longer than its share of the time, and one that
-  // brings the codes AHEAD tiles before.
+  // that a slot is not held longer than its share of the time, and two that
+  // bring the codes AHEAD tiles before.
   static constexpr int CW = F8 ? (NT == 1 ? 8 : 4) : 0;
   static constexpr int TEAM = F8 ? CW / 2 : 1;         // half convert keys, half values
   static constexpr int N_LOAD = F8 ? CW : SL;
-  static constexpr int AHEAD = F8 ? (DP == 64 ? 4 : DP == 128 && NT == 1 ? 3 : 2) : 0;
+  static constexpr int AHEAD = F8 ? (DP == 64 || (DP == 128 && NT == 1) ? 4 : 2) : 0;
+  static_assert(AHEAD % 2 == 0, "keys and values have buffers of their own: each is then used by one fetching warp and one team, in order");
   static constexpr int RAW = BN * DP;                  // bytes of a tile's codes
   // A tile of at most 32 rows, NT = 1 and 128 keys: see k_attend.
   static constexpr bool FEW = NT == 1 && BN == 128;
-  static constexpr int W_LOAD = NT * 4, W_FETCH = W_LOAD + N_LOAD, W_MMA = W_FETCH + (F8 ? 1 : 0);
+  static constexpr int W_LOAD = NT * 4, W_FETCH = W_LOAD + N_LOAD, W_MMA = W_FETCH + (F8 ? 2 : 0);
   static constexpr int THREADS = (W_MMA + 1) * 32;
   // TMEM: two S buffers, tile x's (NT = 2) or key tile k's (NT = 1, k mod 2); then O
   static constexpr int T_O = 2 * BN;
@@ -562,7 +563,7 @@ __device__ __forceinline__ bool find_eights(const W& w, Pages& pg, int64_t j0, i
 }
 
 // Single rows. One warp copies a key tile (zeros for a row of -1): bf16 to a ring
-// slot, e4m3 codes to their buffer, blocks of 64 columns with 64-byte rows.
+// slot, e4m3 codes to their buffer, rows of DP bytes.
 template <class S>
 __device__ __forceinline__ void copy_rows(const Args& a, const void* pages, const int* row, uint32_t dst) {
   const int lane = threadIdx.x & 31, D = a.w.c.head_dim;
@@ -589,17 +590,19 @@ __device__ __forceinline__ void copy_rows(const Args& a, const void* pages, cons
       }
     }
   } else {
-    const int q = lane & 3, rl = lane >> 2;        // 16-code chunk of a block's row; row of 8
-    const uint8_t* base = static_cast<const uint8_t*>(pages) + q * 16;
+    constexpr int CPR = S::DP / 16, RPI = 32 / CPR;
+    const int c = lane % CPR;
+    const bool in = c * 16 < D;
+    const uint8_t* base = static_cast<const uint8_t*>(pages) + c * 16;
 #pragma unroll 1
-    for (int n = 0; n < S::DP / 64 * (S::BN / 32); ++n) {
-      const int cb = n / (S::BN / 32), p = n % (S::BN / 32), mine = pick(p);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int cr = __shfl_sync(0xffffffffu, mine, k * 8 + rl);
-        const bool on = cr >= 0 && cb * 64 + q * 16 < D;
-        copy16(dst + (cb * S::BN + p * 32 + k * 8) * 64 + lane * 16,
-               on ? base + (int64_t)cr * D + cb * 64 : (const void*)a.q, on ? 16 : 0);
+    for (int p = 0; p < S::BN / 32; ++p) {
+      const int mine = pick(p);
+#pragma unroll 8
+      for (int it = 0; it < 32 / RPI; ++it) {
+        const int r = it * RPI + lane / CPR;
+        const int cr = __shfl_sync(0xffffffffu, mine, r);
+        const bool on = in && cr >= 0;
+        copy16(dst + (p * 32 + r) * S::DP + c * 16, on ? base + (int64_t)cr * D : (const void*)a.q, on ? 16 : 0);
       }
     }
   }
@@ -609,16 +612,16 @@ __device__ __forceinline__ void copy_rows(const Args& a, const void* pages, cons
 // last used the buffer has fenced its ordinary accesses.)
 template <class S>
 __device__ __forceinline__ void copy_boxes(const Args& a, const CUtensorMap* map, int eight, uint32_t dst, uint64_t* bar) {
-  constexpr int NB = S::DP / 64;
+  constexpr int NB = S::F8 ? 1 : S::DP / 64;       // copies side by side: 64 columns of bf16, whole rows of codes
   const int lane = threadIdx.x & 31;
-  const int run = lane / NB * a.box, cb = lane % NB;            // the lane's rows and 64-column block
+  const int run = lane / NB * a.box, cb = lane % NB;            // the lane's rows and columns
   const int first = __shfl_sync(0xffffffffu, eight, (run >> 3) & 31);   // (a run lies in one page, its head before the end)
   if (lane == 0) mbar_expect_tx(bar, S::BN * S::DP * (S::F8 ? 1 : 2));
   __syncwarp();
   if (run < S::BN)
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-            dst + (cb * S::BN + run) * (S::F8 ? 64 : 128)),
+            S::F8 ? dst + run * S::DP : dst + (cb * S::BN + run) * 128),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(cb * 64), "r"(first)
         : "memory");
   __syncwarp();
@@ -673,20 +676,19 @@ __device__ __forceinline__ void query_boxes(const W& w, const CUtensorMap* map, 
 // conversions and products or 60 integer instructions for 16 codes.)
 template <class S>
 __device__ __forceinline__ void convert(const uint8_t* exps, int r0, uint32_t src, uint32_t slot) {
-  constexpr int RW = S::BN / S::TEAM, K = RW < 32 ? RW / 8 : 4, NB = S::DP / 64;
-  const int lane = threadIdx.x & 31, q = lane & 3, rl = lane >> 2;
-  const uint32_t c0 = ((2 * q) ^ rl) << 4, c1 = ((2 * q + 1) ^ rl) << 4;
+  constexpr int CPR = S::DP / 16, RPI = 32 / CPR, N = S::BN / S::TEAM / RPI;   // 16-code chunks of a row, rows at a time
+  constexpr int K = N < 4 ? N : 4;
+  const int lane = threadIdx.x & 31, q = lane % CPR, cb = q >> 2;
 #pragma unroll 1
-  for (int end = r0 + RW; r0 < end; r0 += 8 * K) {
-  float scale[K];                                    // any byte is an exponent, also in rows never written
-#pragma unroll
-  for (int k = 0; k < K; ++k) scale[k] = __uint_as_float(max(1u, min(254u, (uint32_t)exps[r0 + k * 8 + rl])) << 23);
-#pragma unroll
-  for (int cb = 0; cb < NB; ++cb) {
-    const uint32_t from = src + (cb * S::BN + r0) * 64 + lane * 16, to = slot + cb * (S::BN * 128) + (r0 + rl) * 128;
+  for (int n = 0; n < N; n += K) {
+    const int r = r0 + n * RPI + lane / CPR;
     uint4 v[K];
+    float scale[K];                                  // any byte is an exponent, also in rows never written
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = ld_shared(from + k * 512);
+    for (int k = 0; k < K; ++k) {
+      v[k] = ld_shared(src + (r + k * RPI) * S::DP + q * 16);
+      scale[k] = __uint_as_float(max(1u, min(254u, (uint32_t)exps[r + k * RPI])) << 23);
+    }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
@@ -696,10 +698,15 @@ __device__ __forceinline__ void convert(const uint8_t* exps, int r0, uint32_t sr
         o[2 * t] = codes_to_bf16(x[t], scale[k]);
         o[2 * t + 1] = codes_to_bf16(x[t] >> 16, scale[k]);
       }
-      st_shared(to + k * 1024 + c0, make_uint4(o[0], o[1], o[2], o[3]));
-      st_shared(to + k * 1024 + c1, make_uint4(o[4], o[5], o[6], o[7]));
+      // 8 neighbouring lanes write all 8 chunks' places of the swizzle: lanes of an
+      // odd block take their second chunk first
+      const uint32_t to = slot + cb * (S::BN * 128) + (r + k * RPI) * 128;
+      const uint32_t c0 = 2 * (q & 3), sw = (r + k * RPI) & 7;
+      const bool odd = cb & 1;
+      const uint4 a0 = make_uint4(o[0], o[1], o[2], o[3]), a1 = make_uint4(o[4], o[5], o[6], o[7]);
+      st_shared(to + (((c0 + (odd ? 1 : 0)) ^ sw) << 4), odd ? a1 : a0);
+      st_shared(to + (((c0 + (odd ? 0 : 1)) ^ sw) << 4), odd ? a0 : a1);
     }
-  }
   }
 }
 
@@ -1224,11 +1231,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       }
       drain_queries();
       if (landing) wait(&sy.full[part], (e / S::SL - 1) & 1, sy, a, false);
-    } else if (warp == S::W_FETCH) {
-      // codes and exponents, AHEAD tiles before they are converted
+    } else if (warp >= S::W_FETCH) {
+      // codes and exponents, AHEAD tiles before they are converted: a warp for the keys', one for the values'
+      const uint32_t mine = warp - S::W_FETCH;
       for (; w.more() && ok; w.next()) {
         const uint32_t n = 2 * (uint32_t)(w.te - w.tb);
-        for (; e - e0 < n; ++e) {
+        for (e = e0 + mine; e - e0 < n; e += 2) {
           const uint32_t at = e % S::AHEAD, dst = codes0 + at * S::RAW;
           const bool kv = (e - e0) & 1;
           const uint8_t* exps = kv ? a.w.c.v_exp : a.w.c.k_exp;
@@ -1258,7 +1266,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       }
       // as above: of the last AHEAD tiles
       for (uint32_t x = e > S::AHEAD ? e - S::AHEAD : 0; x < e; ++x)
-        wait(&sy.raw[x % S::AHEAD], (x / S::AHEAD) & 1, sy, a, false);
+        if ((x & 1) == mine) wait(&sy.raw[x % S::AHEAD], (x / S::AHEAD) & 1, sy, a, false);
     } else {
       // half of the warps on the keys, half on the values, each its own rows
       constexpr int RW = BN / S::TEAM;
@@ -1519,8 +1527,8 @@ cudaError_t launch(Args a, int ctas, cudaStream_t s) {
   if (S::F8 && (reinterpret_cast<uintptr_t>(c.k_exp) | reinterpret_cast<uintptr_t>(c.v_exp)) % 8) a.box = 0;
   alignas(64) CUtensorMap maps[2] = {};
   const uint64_t rows = (uint64_t)c.pages * c.kv_heads * c.page_size;
-  if (a.box && (!tc_encode_2d_rows(&maps[0], c.k, c.head_dim, rows, 64, a.box, S::F8) ||
-                !tc_encode_2d_rows(&maps[1], c.v, c.head_dim, rows, 64, a.box, S::F8)))
+  if (a.box && (!tc_encode_2d_rows(&maps[0], c.k, c.head_dim, rows, S::F8 ? S::DP : 64, a.box, S::F8) ||
+                !tc_encode_2d_rows(&maps[1], c.v, c.head_dim, rows, S::F8 ? S::DP : 64, a.box, S::F8)))
     return cudaErrorInvalidValue;
   // queries: dimensions (column, head, token); a dimension of one takes any stride
   const int64_t hs = a.q_heads > 1 ? a.q_hs : c.head_dim, ts = a.w.b.tokens > 1 ? a.q_ts : a.q_heads * hs;
