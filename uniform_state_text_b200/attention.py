@@ -216,7 +216,7 @@ class KVCache:
                 or out.get_device() != index:
             raise ValueError("out must be contiguous bfloat16 of q's shape")
         if lse is None:
-            lse = torch.empty((tokens, hq), dtype=torch.float32, device=self.device)
+            lse = q.new_empty((tokens, hq), dtype=torch.float32)
         elif lse.dtype is not torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous() \
                 or lse.get_device() != index:
             raise ValueError("lse must be contiguous float32 [tokens, q_heads]")
@@ -224,7 +224,7 @@ class KVCache:
         n = self._scratch.get(key)
         if n is None:
             n = self._scratch[key] = dg_cache_attention_scratch_bytes(c, batch.c, hq)
-        scratch = torch.empty(n, dtype=torch.uint8, device=self.device)
+        scratch = self.status.new_empty((n // 4,))
         _call(index, dg_cache_attention, c, batch.c, hq, q.data_ptr(), *qs,
               c.head_dim ** -0.5 if scale is None else scale, mask, tree_ptr, words, out.data_ptr(),
               lse.data_ptr(), scratch.data_ptr(), n)

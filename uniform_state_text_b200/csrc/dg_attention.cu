@@ -41,6 +41,7 @@
 // one in use (P then stays below 2^8, harmless in bf16 and fp32): the wait for
 // the previous P V and the pass over O are rare.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <type_traits>
 
@@ -128,7 +129,7 @@ struct Shape {
   static constexpr int THREADS = (W_MMA + 1) * 32;
   // TMEM: two S buffers, tile x's (NT = 2) or key tile k's (NT = 1, k mod 2); then O
   static constexpr int T_O = 2 * BN;
-  static constexpr size_t SMEM = 1024 + (size_t)NT * QTILE + (size_t)SL * SLOT + (size_t)AHEAD * RAW + (FEW ? 4 * 32 * 64 + 4 * 32 * 8 : 0) + 1024;
+  static constexpr size_t SMEM = 1024 + (size_t)NT * QTILE + (size_t)SL * SLOT + (size_t)AHEAD * RAW + (FEW ? 2 * 4 * 32 * 64 + 4 * 32 * 8 : 0) + 1024;
   static_assert(8 * (kMaxBatch + 1) <= SL * SLOT, "the plan's sums lie in the ring before it is used");
   static_assert(T_O + NT * DP <= TMEM_COLS, "TMEM");
   static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -814,8 +815,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
   unsigned char* codes = ring + S::SL * S::SLOT;
   Sync& sy = *reinterpret_cast<Sync*>(codes + S::AHEAD * S::RAW);
   static_assert(sizeof(Sync) <= 1024 && S::SL <= 8 && S::N_LOAD <= 8 && S::AHEAD <= 4, "barriers");
-  float* few_o = reinterpret_cast<float*>(codes + S::AHEAD * S::RAW + 1024);         // [4][32][16]
-  float2* few_ml = reinterpret_cast<float2*>(few_o + 4 * 32 * 16);              // [4][32]
+  float* few_o = reinterpret_cast<float*>(codes + S::AHEAD * S::RAW + 1024);         // two of [4][32][16]
+  float2* few_ml = reinterpret_cast<float2*>(few_o + 2 * 4 * 32 * 16);              // [4][32]
   int64_t* pref = reinterpret_cast<int64_t*>(ring);
   constexpr int ROWS = S::NT * 128, BN = S::BN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1016,8 +1017,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       const int64_t prow = (int64_t)piece * a.rows + rr;
       tc_fence_after();
       if (S::FEW && few) {
-        // join the four copies: m and l through shared memory, O in chunks of 16 columns;
-        // thread (row, 4 columns) adds the copies
+        // join the four copies: m and l through shared memory, O in chunks of 16 columns
+        // in two buffers by turns; thread (row, 4 columns) adds the copies
         auto meet = [&]() {
           __syncwarp();
           if (lane == 0) mbar_arrive(&sy.merge);
@@ -1045,16 +1046,17 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
 #pragma unroll 1
         for (int c = 0; c < S::DP / 16; ++c) {
           uint32_t o[16];
+          float* const stage = few_o + (c & 1) * (4 * 32 * 16);
           tmem_ld16(t_o + c * 16, o);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(few_o + (quarter * 32 + lane) * 16 + ((k + lane) & 3) * 4) =
+            *reinterpret_cast<uint4*>(stage + (quarter * 32 + lane) * 16 + ((k + lane) & 3) * 4) =
                 make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           if (!meet()) { ok = false; break; }
           float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float4 u = *reinterpret_cast<const float4*>(few_o + (k * 32 + fr) * 16 + (((t & 3) + fr) & 3) * 4);
+            const float4 u = *reinterpret_cast<const float4*>(stage + (k * 32 + fr) * 16 + (((t & 3) + fr) & 3) * 4);
             v[0] = fmaf(u.x, f[k], v[0]);
             v[1] = fmaf(u.y, f[k], v[1]);
             v[2] = fmaf(u.z, f[k], v[2]);
@@ -1075,8 +1077,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
               *reinterpret_cast<uint2*>(a.out + (int64_t)frow * a.w.c.head_dim + c * 16 + fc) =
                   make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
           }
-          if (!meet()) { ok = false; break; }
         }
+        // (the first meeting of the next item is behind the last of these reads)
         if (!ok) break;
         if (on && fc == 0) {
           if (!whole) a.part_ml[(int64_t)piece * a.rows + fr] = make_float2(fm, fl);
@@ -1518,7 +1520,7 @@ Plan make_plan(const dg_kv_cache& c, const dg_kv_batch& b, int q_heads) {
 }
 
 template <class S>
-cudaError_t launch(Args a, int ctas, cudaStream_t s) {
+cudaError_t launch(Args a, int dev, int ctas, cudaStream_t s) {
   // TMA copies take runs of rows that lie together: a power of two that divides
   // page_size, at least 8 (one swizzle pattern, and the exponents' 8 bytes)
   const dg_kv_cache& c = a.w.c;
@@ -1540,8 +1542,13 @@ cudaError_t launch(Args a, int ctas, cudaStream_t s) {
     const uint32_t box[3] = {64, (uint32_t)a.G, 32 / (uint32_t)a.G};
     if (!tc_encode_3d_bf16(&q_map, a.q, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(k_attend<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  static std::atomic<uint64_t> ready{0};                // devices whose kernel may take this much shared memory
+  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(k_attend<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
   k_attend<S><<<ctas, S::THREADS, S::SMEM, s>>>(a, maps[0], maps[1], q_map);
   if ((e = cudaGetLastError()) != cudaSuccess || ctas == 1) return e;
   // the join's launch overlaps the kernel's end; it waits for it on the device
@@ -1550,7 +1557,7 @@ cudaError_t launch(Args a, int ctas, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   // no more than ctas - 1 items are cut, whatever the lengths; as many blocks as fit at once
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(6ll * ctas, (int64_t)(ctas - 1) * a.rows));
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(6ll * ctas, (int64_t)(ctas - 1) * ((a.rows + 7) / 8)));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cfg.attrs = at;
@@ -1623,7 +1630,7 @@ extern "C" int dg_cache_attention(const dg_kv_cache* cache, const dg_kv_batch* b
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto go = [&](auto dp, auto nt) {
     constexpr int DP = decltype(dp)::value, NT = decltype(nt)::value;
-    return f8 ? launch<Shape<DP, NT, true>>(a, ctas, s) : launch<Shape<DP, NT, false>>(a, ctas, s);
+    return f8 ? launch<Shape<DP, NT, true>>(a, dev, ctas, s) : launch<Shape<DP, NT, false>>(a, dev, ctas, s);
   };
   using std::integral_constant;
   const integral_constant<int, 1> one;
