@@ -341,6 +341,55 @@ def test_attention_long(fmt, D, Hk, G, page, mask, lengths):
                      rows=[0, 1, 15, 16, 31, 32, 63, 64, 100, 127, 128, 129, 199, 255, 256, 299, 511, 514, 599])
 
 
+@pytest.mark.parametrize("fmt,D,Hk,G,page,mask,lengths", [
+    (dg.DG_KV_E4M3, 64, 2, 4, 8, "full", [(200, 256), (30, 100)]),         # two row tiles, codes
+    (dg.DG_KV_E4M3, 128, 1, 2, 16, "causal", [(0, 700), (131, 400)]),
+    (dg.DG_KV_E4M3, 96, 1, 6, 256, "tree", [(900, 61), (0, 90)]),          # G no power of two
+    (dg.DG_KV_BF16, 64, 1, 64, 256, "causal", [(500, 9)]),                 # G above 32
+    (dg.DG_KV_BF16, 128, 2, 12, 24, "tree", [(77, 40), (500, 33)]),
+    (dg.DG_KV_BF16, 128, 3, 1, 128, "full", [(383, 129), (1, 513)]),
+    (dg.DG_KV_BF16, 208, 1, 2, 64, "causal", [(70, 300)]),
+    (dg.DG_KV_E4M3, 48, 1, 3, 16, "causal", [(300, 150)])])                # below 64: rows one by one
+def test_attention_more_shapes(fmt, D, Hk, G, page, mask, lengths):
+    s = Setup(lengths, fmt, Hk, D, page, seed=D + page)
+    q = _tokens_q(s, G, 4)
+    words = _tree(s.new, 8, empty=(3, 50)) if mask == "tree" else None
+    tree = torch.from_numpy(words.view(np.int32)).cuda() if mask == "tree" else None
+    out, lse = s.cache.attend(q, s.batch, MASKS[mask], tree=tree)
+    s.cache.check()
+    _check_attention(s, q, mask, D ** -0.5, out, lse, words)
+
+
+def test_attention_of_the_largest_batch():
+    s = Setup([(b % 37, 1 + (b % 5 == 0)) for b in range(1024)], dg.DG_KV_BF16, 1, 64, 16, seed=1)
+    q = _tokens_q(s, 2)
+    out, lse = s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL)
+    s.cache.check()
+    _check_attention(s, q, "causal", 0.125, out, lse)
+    big = dg.KVBatch(torch.zeros(1025, 1, dtype=torch.int32, device="cuda"),
+                     torch.zeros(1026, dtype=torch.int32, device="cuda"),
+                     torch.zeros(1025, dtype=torch.int32, device="cuda"), s.tokens)
+    with pytest.raises(dg.DgError):
+        s.cache.attend(q, big, dg.DG_MASK_CAUSAL)
+
+
+@pytest.mark.parametrize("kexp,vexp", [(-20, 30), (25, -40), (60, 90)])
+def test_attention_over_rows_of_extreme_scale(kexp, vexp):
+    """Exponents far from zero, beyond the range of fp16."""
+    s = Setup([(150, 3), (20, 1)], dg.DG_KV_E4M3, 2, 128, 16, seed=2)
+    for b in range(2):
+        n = s.past[b] + s.new[b]
+        rows = dg.KVBatch(s.table[b:b + 1].contiguous(), torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+                          torch.zeros(1, dtype=torch.int32, device="cuda"), n)
+        kv = torch.randn(2, n, 2, 128, generator=s.g, device="cuda")
+        kv[1] *= torch.exp2(torch.randint(-6, 7, (n, 2, 1), generator=s.g, device="cuda").float())
+        s.cache.write(kv[0] * 2.0 ** kexp, kv[1] * 2.0 ** vexp, rows)
+    q = (_tokens_q(s, 4, 5).float() * 2.0 ** -kexp).bfloat16()
+    out, lse = s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL)
+    s.cache.check()
+    _check_attention(s, q, "causal", 128 ** -0.5, out, lse)
+
+
 def test_attention_large_logits_and_growing_maxima():
     """Logits up to hundreds, rising along the keys, so that the running maximum moves often."""
     s = Setup([(1000, 3)], dg.DG_KV_BF16, 1, 64, 16, seed=8)
@@ -453,6 +502,25 @@ def test_attention_is_repeatable_and_keeps_nothing_in_its_scratch():
                               128 ** -0.5, dg.DG_MASK_CAUSAL, 0, 0, out.data_ptr(), 0,
                               scratch.data_ptr(), n, torch.cuda.current_stream().cuda_stream)
         assert same(a, out)
+
+
+@pytest.mark.parametrize("fmt", [dg.DG_KV_BF16, dg.DG_KV_E4M3])
+@pytest.mark.parametrize("D,G,page,mask,lengths", [
+    (128, 4, 64, "causal", [(3000 - 91 * b, 1) for b in range(33)]), (64, 8, 16, "causal", [(2500, 1), (9000, 1)]),
+    (256, 2, 32, "full", [(1500, 128), (700, 100)]), (128, 2, 16, "causal", [(0, 1500), (200, 900)]),
+    (64, 4, 128, "full", [(900, 300)]), (128, 3, 5, "causal", [(400, 200), (3000, 1)])])
+def test_repeated_calls_agree_to_the_bit(fmt, D, G, page, mask, lengths):
+    """Hand-overs between warps that went wrong now and then would show here."""
+    s = Setup(lengths, fmt, 4, D, page, seed=D + G)
+    q = _tokens_q(s, G, 2)
+    want, lse = s.cache.attend(q, s.batch, MASKS[mask])
+    off = torch.zeros((), dtype=torch.int64, device="cuda")
+    bits, lbits = want.view(torch.int16), lse.view(torch.int32)
+    for _ in range(60):
+        out, l = s.cache.attend(q, s.batch, MASKS[mask])
+        off += (out.view(torch.int16) != bits).sum() + (l.view(torch.int32) != lbits).sum()
+    assert int(off) == 0
+    s.cache.check()
 
 
 def test_captured_graph_follows_the_lengths():
