@@ -24,22 +24,40 @@
 // A CTA's warps:
 //   softmax   NT x 4 warps: TMEM lane = row; S from TMEM, P = 2^(t - m) back
 //             to TMEM as bf16, the running m and l in registers
-//   loads     one or two warps per slot of the ring of key and value tiles:
-//             runs of rows that lie together in a page by TMA, or single rows
-//             by 16-byte cp.async, into the 128-byte swizzle that the MMA
-//             reads; e4m3 codes are converted to bf16, which holds code x 2^e
-//             exactly
-//             exactly. Each also brings its share of an item's query rows,
-//             after its first tile of the item
-//   MMA       one thread: S = Q K^T (both from shared memory), O += P V (P from
-//             TMEM, V as it lies, keys along K), accumulators in TMEM
+//   loads     bf16: one warp per slot of the ring of key and value tiles; runs
+//             of rows that lie together in a page come by TMA, single rows by
+//             16-byte cp.async, into the 128-byte swizzle that the MMA reads.
+//             e4m3: two warps bring the codes ahead of their use, others convert
+//             them to bf16, which holds code x 2^e exactly. The item's query
+//             rows come by TMA where a head's group is a power of two
+//   MMA       one warp, one elected lane issuing: S = Q K^T (both from shared
+//             memory), O += P V (P from TMEM, V as it lies, keys along K),
+//             accumulators in TMEM
 // With NT = 2 the two tiles share each key and value tile and alternate, so
 // that one tile's softmax runs under the other's products; with NT = 1 there
-// are two S buffers and S of the next tile is issued before P V of this one.
+// are two S buffers and S of the next keys is issued before P V of these. (With
+// two buffers for each of two tiles, TMEM has room for 64 keys to a tile only:
+// the prompt below then took 456 us for 347, a tile's hand-overs costing as
+// much as with 128.)
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 over the
 // one in use (P then stays below 2^8, harmless in bf16 and fp32): the wait for
-// the previous P V and the pass over O are rare.
+// the previous P V and the pass over O are rare. Without that the prompt took
+// 333 us for 293.
+//
+// Rounding: keys, values and queries enter the products as they are; P is
+// rounded to bf16, the tensor cores' operand type with V's range (2^-9 relative,
+// independent from key to key); S, m, l and O stay in fp32; the output is
+// rounded once.
+//
+// Measured on B200 (calls in turn on the device, two sets of inputs):
+//   one token, 131072 bf16 keys, 8 x 2 heads of 128: 96 us, 5.6 TB/s of the 6.55
+//     that a copy reaches; bound by memory
+//   33 tokens, 2000 to 8000 e4m3 keys each, 8 x 4 heads of 128: 140 us, 2.1
+//     TB/s; bound by the instructions that convert codes and by hand-overs
+//   4 canvases of 256, 8448 e4m3 keys, 4 x 2 heads of 256: 131 us, 540 TFLOP/s
+//   a prompt of 8192, 8 x 2 heads of 128: 290 us, 950 TFLOP/s; bound by the
+//     chain softmax - P V - S of each tile, the tensor cores busy half the time
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -113,7 +131,7 @@ struct Shape {
   static constexpr int BN = DP == 256 ? 64 : 128;      // keys per tile
   static constexpr int SLOT = BN * DP * 2;
   static constexpr int QTILE = 128 * DP * 2;
-  static constexpr int SL = F8 ? (DP == 64 ? 6 : DP == 128 && NT == 1 ? 3 : 4) : DP == 256 ? 4 : DP == 128 ? 5 : (NT == 2 ? 6 : 8);   // ring slots
+  static constexpr int SL = F8 ? (DP == 64 ? 6 : 4) : DP == 256 ? 4 : DP == 128 ? 5 : (NT == 2 ? 6 : 8);   // ring slots
   // Load warps. bf16: one per slot. e4m3: CW that convert, several to a tile, so
   // that a slot is not held longer than its share of the time, and two that
   // bring the codes AHEAD tiles before.
@@ -123,13 +141,11 @@ struct Shape {
   static constexpr int AHEAD = F8 ? (DP == 64 || (DP == 128 && NT == 1) ? 4 : 2) : 0;
   static_assert(AHEAD % 2 == 0, "keys and values have buffers of their own: each is then used by one fetching warp and one team, in order");
   static constexpr int RAW = BN * DP;                  // bytes of a tile's codes
-  // A tile of at most 32 rows, NT = 1 and 128 keys: see k_attend.
-  static constexpr bool FEW = NT == 1 && BN == 128;
   static constexpr int W_LOAD = NT * 4, W_FETCH = W_LOAD + N_LOAD, W_MMA = W_FETCH + (F8 ? 2 : 0);
   static constexpr int THREADS = (W_MMA + 1) * 32;
   // TMEM: two S buffers, tile x's (NT = 2) or key tile k's (NT = 1, k mod 2); then O
   static constexpr int T_O = 2 * BN;
-  static constexpr size_t SMEM = 1024 + (size_t)NT * QTILE + (size_t)SL * SLOT + (size_t)AHEAD * RAW + (FEW ? 2 * 4 * 32 * 64 + 4 * 32 * 8 : 0) + 1024;
+  static constexpr size_t SMEM = 1024 + (size_t)NT * QTILE + (size_t)SL * SLOT + (size_t)AHEAD * RAW + 1024;
   static_assert(8 * (kMaxBatch + 1) <= SL * SLOT, "the plan's sums lie in the ring before it is used");
   static_assert(T_O + NT * DP <= TMEM_COLS, "TMEM");
   static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -303,7 +319,6 @@ struct Sync {
   uint64_t raw[8], taken[4];       // e4m3: a tile's codes have landed, and have been converted (bf16: a value
                                    // tile to be cleaned has landed)
   uint8_t exps[4][128];            // their rows' exponents
-  uint64_t merge;                  // between the four warps that share a tile's rows
   uint32_t tmem;
   int abort, nonfinite;
   Start start;
@@ -357,18 +372,8 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// 16 columns of TMEM to each lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-// The same in two halves: the issue (its registers are not to be read yet), and
-// the wait, which names them so that no read moves above it.
+// 16 columns of TMEM to each lane, in two halves: the issue (its registers are
+// not to be read yet), and the wait, which names them so that no read moves above it.
 __device__ __forceinline__ void tmem_ld16_issue(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -634,7 +639,6 @@ __device__ __forceinline__ void load_queries(const W& w, int part, uint32_t dst)
   constexpr int CPR = S::DP / 8, RPI = 32 / CPR, ROWS = S::NT * 128;
   const Args& a = w.a;
   const int lane = threadIdx.x & 31, c = lane % CPR, rows = w.rows();
-  const bool few = S::FEW && rows <= 32;
 #pragma unroll 4
   for (int r0 = part * RPI; r0 < rows; r0 += S::N_LOAD * RPI) {
     const int r = r0 + lane / CPR;
@@ -643,8 +647,6 @@ __device__ __forceinline__ void load_queries(const W& w, int part, uint32_t dst)
     const bool on = r < rows && c * 8 < a.w.c.head_dim;
     const __nv_bfloat16* src = on ? a.q + (int64_t)(w.t0 + i) * a.q_ts + (int64_t)(w.h * a.G + g) * a.q_hs + c * 8 : a.q;
     copy16(dst + (r >> 7) * S::QTILE + swizzled(r & 127, c, 128), src, on ? 16 : 0);
-    if (few)
-      for (int k = 32; k < 128; k += 32) copy16(dst + swizzled(r + k, c, 128), src, on ? 16 : 0);
   }
   copies_landed();
 }
@@ -657,12 +659,11 @@ template <class S, typename W>
 __device__ __forceinline__ void query_boxes(const W& w, const CUtensorMap* map, uint32_t dst, uint64_t* bar) {
   constexpr int NB = S::DP / 64, ROWS = S::NT * 128;
   const int lane = threadIdx.x & 31, rows = w.rows();
-  const bool few = S::FEW && rows <= 32;
-  const int group = lane / NB, cb = lane % NB, n = few ? 4 : (rows + 31) / 32;   // groups of 32 rows
+  const int group = lane / NB, cb = lane % NB, n = (rows + 31) / 32;   // groups of 32 rows
   if (lane == 0) mbar_expect_tx(bar, n * NB * 32 * 128);
   __syncwarp();
   if (group < n) {
-    const uint32_t i = w.a.over_g((uint32_t)w.m * ROWS + (few ? 0 : group * 32));
+    const uint32_t i = w.a.over_g((uint32_t)w.m * ROWS + group * 32);
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
             dst + (group >> 2) * S::QTILE + cb * (128 * 128) + (group & 3) * (32 * 128)),
@@ -743,8 +744,8 @@ __device__ __forceinline__ void clean_rows(uint32_t slot, int r0, int live, bool
 
 // o (columns d .. d + 3 of a row's sum) with the infinities and NaN among the
 // values that new token i of the sequence sees in the segment's keys from
-// position `from` on. They decide the result wherever there are any: load_rows
-// has left them out, or a product with P = 0 has made a NaN of them.
+// position `from` on, where clean_rows has left them out. They decide the result
+// wherever there are any.
 template <class S, typename W>
 __device__ __noinline__ float4 with_not_finite(const W w, const uint32_t* tree, int i, int d, int64_t from, float4 o) {
   const Args& a = w.a;
@@ -797,13 +798,6 @@ __device__ __forceinline__ void transpose4(uint4* v) {
 // ---------------------------------------------------------------------------
 // The kernel.
 // ---------------------------------------------------------------------------
-//
-// Few rows. A tile of at most 32 rows (NT = 1, 128 keys) would leave three of
-// the four softmax warps idle and one with all 128 columns. Its rows are laid
-// into the tile four times instead, and warp k takes columns 32 k to 32 k + 31
-// of its copy: P is zero in the others, so that O of copy k is the sum over a
-// quarter of the keys, with an m and l of its own. The four are joined at the
-// end of the item.
 template <class S>
 __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap k_map,
                                                            const __grid_constant__ CUtensorMap v_map,
@@ -815,8 +809,6 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
   unsigned char* codes = ring + S::SL * S::SLOT;
   Sync& sy = *reinterpret_cast<Sync*>(codes + S::AHEAD * S::RAW);
   static_assert(sizeof(Sync) <= 1024 && S::SL <= 8 && S::N_LOAD <= 8 && S::AHEAD <= 4, "barriers");
-  float* few_o = reinterpret_cast<float*>(codes + S::AHEAD * S::RAW + 1024);         // two of [4][32][16]
-  float2* few_ml = reinterpret_cast<float2*>(few_o + 2 * 4 * 32 * 16);              // [4][32]
   int64_t* pref = reinterpret_cast<int64_t*>(ring);
   constexpr int ROWS = S::NT * 128, BN = S::BN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -832,7 +824,6 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     mbar_init(&sy.q_full, a.q_box ? 1 : S::N_LOAD);
     mbar_init(&sy.q_free, 1);
     mbar_init(&sy.fin, 1);
-    mbar_init(&sy.merge, 4);
     for (int x = 0; x < 8; ++x) mbar_init(&sy.raw[x], S::F8 ? 1 + BN / 8 : 1);
     for (int x = 0; x < S::AHEAD; ++x) mbar_init(&sy.taken[x], S::TEAM);
     sy.abort = 0;
@@ -864,14 +855,11 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     uint32_t gt = 0;                                  // key tiles done by this CTA
     auto pv_done = [&](uint32_t k) { return wait_warp(&sy.o_done[4 * x + (k & 3)], (k >> 2) & 1, sy, a); };
     Open open{0, 0, 0, 0, 0};                         // an item begun and not finished
-    uint32_t merges = 0;
     for (; w.more() && ok; w.next()) {
       const int rows = w.rows();
-      const bool few = S::FEW && rows <= 32;
-      const bool any = few || x * 128 + quarter * 32 < rows;     // warp-uniform
-      const int rr = few ? lane : r;                  // row within the item
-      const bool valid = rr < rows;
-      const uint32_t rid = (uint32_t)w.m * ROWS + (valid ? rr : 0);
+      const bool any = x * 128 + quarter * 32 < rows; // warp-uniform
+      const bool valid = r < rows;
+      const uint32_t rid = (uint32_t)w.m * ROWS + (valid ? r : 0);
       const int i = (int)a.over_g(rid), g = (int)(rid - (uint32_t)i * a.G);
       const uint32_t* tree = a.mask == DG_MASK_TREE ? a.tree + (int64_t)(w.t0 + i) * a.words : nullptr;
       // tiles that reach beyond this position hold some that the row may not see
@@ -887,7 +875,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           const bool masked = __any_sync(0xffffffffu, j0 + BN > clear);
           // The usual tile, all columns seen: straight code, the next 16 columns on
           // their way from TMEM while one chunk is worked on.
-          bool plain = !masked && !few;
+          bool plain = !masked;
           uint32_t ra[16], rb[16];
           float top = -INFINITY;
           if (plain) {
@@ -908,12 +896,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
             }
             plain = !__any_sync(0xffffffffu, top != top && valid);    // NaN: below, where it goes by MUFU
           }
-          // chunks of 32 columns: all of them, or this warp's own
-          const int c0 = few ? quarter : 0, c1 = plain ? c0 : few ? quarter + 1 : BN / 32;
+          // others: 32 columns at a time
+          const int chunks = plain ? 0 : BN / 32;
           float s[32];
           if (!plain) top = -INFINITY;
 #pragma unroll 1
-          for (int c = c0; c < c1; ++c) {
+          for (int c = 0; c < chunks; ++c) {
             tmem_ld32(t_s + c * 32, s);
             if (masked) {
               const uint32_t word = seen(w, tree, i, j0 + c * 32);
@@ -975,14 +963,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
             l1 = hi2(ls);
           }
 #pragma unroll 1
-          for (int c = c0; c < c1; ++c) {
-            if (!few) {                               // one chunk is still in registers
-              tmem_ld32(t_s + c * 32, s);
-              if (masked) {
-                const uint32_t word = seen(w, tree, i, j0 + c * 32);
+          for (int c = 0; c < chunks; ++c) {
+            tmem_ld32(t_s + c * 32, s);
+            if (masked) {
+              const uint32_t word = seen(w, tree, i, j0 + c * 32);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) s[j] = (word >> j) & 1 ? s[j] : -INFINITY;
-              }
+              for (int j = 0; j < 32; ++j) s[j] = (word >> j) & 1 ? s[j] : -INFINITY;
             }
             uint32_t p[16];
 #pragma unroll
@@ -994,11 +980,6 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
               p[j >> 1] = pack_bf16(e0, e1);
             }
             tmem_st16(t_s + c * 16, p);
-          }
-          if (S::FEW && few) {
-            const uint32_t zero[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-            for (int c = 1; c < 4; ++c) tmem_st16(t_s + ((quarter + c) & 3) * 16, zero);
           }
           l += l0 + l1;
           tmem_st_wait();
@@ -1014,77 +995,9 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       const bool fix = a.mask != DG_MASK_FULL && *(volatile int*)&sy.nonfinite;
       const int piece = blockIdx.x * 2 + (w.tb == 0 ? 1 : 0);
       const int orow = (w.t0 + i) * a.q_heads + w.h * a.G + g;
-      const int64_t prow = (int64_t)piece * a.rows + rr;
+      const int64_t prow = (int64_t)piece * a.rows + r;
       tc_fence_after();
-      if (S::FEW && few) {
-        // join the four copies: m and l through shared memory, O in chunks of 16 columns
-        // in two buffers by turns; thread (row, 4 columns) adds the copies
-        auto meet = [&]() {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sy.merge);
-          return wait_warp(&sy.merge, merges++ & 1, sy, a);
-        };
-        few_ml[quarter * 32 + lane] = make_float2(m, l);
-        if (!meet()) { ok = false; break; }
-        const int t = quarter * 32 + lane, fr = t >> 2, fc = (t & 3) * 4;
-        float f[4], fm = -INFINITY, fl = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) fm = fmaxf(fm, few_ml[k * 32 + fr].x);
-        const float sub = fm == -INFINITY ? 0.f : fm;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 ml = few_ml[k * 32 + fr];
-          f[k] = ex2(ml.x - sub);
-          fl += f[k] * ml.y;
-        }
-        const bool on = fr < rows;
-        const uint32_t frid = (uint32_t)w.m * ROWS + (on ? fr : 0);
-        const int fi = (int)a.over_g(frid);
-        const int frow = (w.t0 + fi) * a.q_heads + w.h * a.G + (int)(frid - (uint32_t)fi * a.G);
-        const uint32_t* ftree = a.mask == DG_MASK_TREE ? a.tree + (int64_t)(w.t0 + fi) * a.words : nullptr;
-        const float inv = fl > 0.f ? 1.f / fl : fl == 0.f ? 0.f : fl;
-#pragma unroll 1
-        for (int c = 0; c < S::DP / 16; ++c) {
-          uint32_t o[16];
-          float* const stage = few_o + (c & 1) * (4 * 32 * 16);
-          tmem_ld16(t_o + c * 16, o);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(stage + (quarter * 32 + lane) * 16 + ((k + lane) & 3) * 4) =
-                make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          if (!meet()) { ok = false; break; }
-          float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float4 u = *reinterpret_cast<const float4*>(stage + (k * 32 + fr) * 16 + (((t & 3) + fr) & 3) * 4);
-            v[0] = fmaf(u.x, f[k], v[0]);
-            v[1] = fmaf(u.y, f[k], v[1]);
-            v[2] = fmaf(u.z, f[k], v[2]);
-            v[3] = fmaf(u.w, f[k], v[3]);
-          }
-          if (on) {
-            // (the copies that do not take a key multiply its value by zero)
-            const bool off = !(fabsf(v[0]) + fabsf(v[1]) + fabsf(v[2]) + fabsf(v[3]) < INFINITY);
-            if (fix || off) {
-              const float4 u = with_not_finite<S>(w, ftree, fi, c * 16 + fc, off ? 0 : w.clear() / BN * BN,
-                                                  make_float4(v[0], v[1], v[2], v[3]));
-              v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-            }
-            if (!whole)
-              *reinterpret_cast<float4*>(a.part_o + ((int64_t)piece * a.rows + fr) * S::DP + c * 16 + fc) =
-                  make_float4(v[0], v[1], v[2], v[3]);
-            else if (c * 16 < a.w.c.head_dim)
-              *reinterpret_cast<uint2*>(a.out + (int64_t)frow * a.w.c.head_dim + c * 16 + fc) =
-                  make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
-          }
-        }
-        // (the first meeting of the next item is behind the last of these reads)
-        if (!ok) break;
-        if (on && fc == 0) {
-          if (!whole) a.part_ml[(int64_t)piece * a.rows + fr] = make_float2(fm, fl);
-          else if (a.lse) a.lse[frow] = fl == 0.f ? -INFINITY : (fm + log2f(fl)) * kLn2;
-        }
-      } else if (any) {
+      if (any) {
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
         // stores by fours of lanes, 64 contiguous bytes of a row each
         const int four = lane & ~3, q = lane & 3;
@@ -1128,7 +1041,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
               transpose4(v);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                if (rr - q + k < rows)
+                if (r - q + k < rows)
                   *reinterpret_cast<uint4*>(a.part_o + (prow - q + k) * S::DP + c * 32 + h * 16 + q * 4) = v[k];
             }
           }
