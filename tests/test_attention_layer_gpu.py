@@ -360,6 +360,35 @@ def test_attention_more_shapes(fmt, D, Hk, G, page, mask, lengths):
     _check_attention(s, q, mask, D ** -0.5, out, lse, words)
 
 
+@pytest.mark.parametrize("D", [64, 48])                  # queries by TMA, and row by row
+def test_other_orders_of_the_rows(D):
+    """Heads outermost, every other token of a buffer, and one row shared by all heads."""
+    lengths, Hk, G = [(30, 40), (3, 7)], 2, 4
+    s = Setup(lengths, dg.DG_KV_E4M3, Hk, D, 16, seed=D, fill=False)
+    n = s.tokens
+    kv = torch.randn(2, Hk, 2 * n, D, generator=s.g, device="cuda").bfloat16()
+    k, v = kv[0, :, ::2].transpose(0, 1), kv[1, :, 1::2].transpose(0, 1)
+    for b, (p, _) in enumerate(lengths):
+        s.put(b, torch.randn(2, p, Hk, D, generator=s.g, device="cuda"))
+    s.cache.write(k, v, s.batch)
+    back = s.cache.read(s.batch, torch.float32)
+    s2 = Setup(lengths, dg.DG_KV_E4M3, Hk, D, 16, seed=D, fill=False)
+    s2.cache.write(k.contiguous(), v.contiguous(), s2.batch)
+    for x, y in zip(back, s2.cache.read(s2.batch, torch.float32)):
+        assert torch.equal(x, y)
+    heads_outer = torch.randn(Hk * G, n, D, generator=s.g, device="cuda").bfloat16().transpose(0, 1)
+    shared = heads_outer[:, :1].expand(-1, Hk * G, -1)
+    for q in (heads_outer, shared):
+        out, lse = s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL)
+        _check_attention(s, q, "causal", D ** -0.5, out, lse)
+    pos, freq = torch.arange(n, device="cuda").int(), dg.rope_frequencies(32)
+    a, b = dg.qk_norm_rope(heads_outer, k, None, None, pos, freq)
+    _check_norm(heads_outer, a, None, pos, freq, False, 1e-6, 0.0, U16)
+    _check_norm(k, b, None, pos, freq, False, 1e-6, 0.0, U16)
+    with pytest.raises(ValueError):
+        s.cache.attend(heads_outer.transpose(1, 2), s.batch, dg.DG_MASK_CAUSAL)
+
+
 def test_attention_of_the_largest_batch():
     s = Setup([(b % 37, 1 + (b % 5 == 0)) for b in range(1024)], dg.DG_KV_BF16, 1, 64, 16, seed=1)
     q = _tokens_q(s, 2)
