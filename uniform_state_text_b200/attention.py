@@ -178,7 +178,7 @@ class KVCache:
         code = _dtype(dtype)
         if out is None:
             shape = (batch.tokens, c.kv_heads, c.head_dim)
-            k, v = (torch.empty(shape, dtype=dtype, device=self.device) for _ in "kv")
+            k, v = self.k.new_empty(shape, dtype=dtype), self.k.new_empty(shape, dtype=dtype)
         else:
             k, v = out
             for t in (k, v):

@@ -53,8 +53,8 @@
 // Measured on B200 (calls in turn on the device, two sets of inputs):
 //   one token, 131072 bf16 keys, 8 x 2 heads of 128: 96 us, 5.6 TB/s of the 6.55
 //     that a copy reaches; bound by memory
-//   33 tokens, 2000 to 8000 e4m3 keys each, 8 x 4 heads of 128: 140 us, 2.1
-//     TB/s; bound by the instructions that convert codes and by hand-overs
+//   33 tokens, 2000 to 8000 e4m3 keys each, 8 x 4 heads of 128: 129 us, 2.2
+//     TB/s; bound by hand-overs between the warps, tile by tile
 //   4 canvases of 256, 8448 e4m3 keys, 4 x 2 heads of 256: 131 us, 540 TFLOP/s
 //   a prompt of 8192, 8 x 2 heads of 128: 290 us, 950 TFLOP/s; bound by the
 //     chain softmax - P V - S of each tile, the tensor cores busy half the time
@@ -134,8 +134,10 @@ struct Shape {
   static constexpr int SL = F8 ? (DP == 64 ? 6 : 4) : DP == 256 ? 4 : DP == 128 ? 5 : (NT == 2 ? 6 : 8);   // ring slots
   // Load warps. bf16: one per slot. e4m3: CW that convert, several to a tile, so
   // that a slot is not held longer than its share of the time, and two that
-  // bring the codes AHEAD tiles before.
-  static constexpr int CW = F8 ? (NT == 1 ? 8 : 4) : 0;
+  // bring the codes AHEAD tiles before. (The 33 single tokens above: 129 us with
+  // 4, 137 with 8, 215 with 2; the canvases, whose rows are twice as long: 146
+  // and 131.)
+  static constexpr int CW = F8 ? (DP == 256 ? 8 : 4) : 0;
   static constexpr int TEAM = F8 ? CW / 2 : 1;         // half convert keys, half values
   static constexpr int N_LOAD = F8 ? CW : SL;
   static constexpr int AHEAD = F8 ? (DP == 64 || (DP == 128 && NT == 1) ? 4 : 2) : 0;
