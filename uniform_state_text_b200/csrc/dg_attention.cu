@@ -1099,7 +1099,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     auto position = [&]() { return (int64_t)(w.tb + (int)((e - e0) >> 1)) * BN; };
     // of entry e: its rows before the sequence's end; whether it holds values that not every row of the item sees
     auto live_rows = [&]() { return (int)min((int64_t)BN, w.keys() - position()); };
-    auto to_scrub = [&]() { return ((e - e0) & 1) && a.mask != DG_MASK_FULL && position() + BN > w.clear(); };
+    // (not behind the end: a single token's last tile has none)
+    auto to_scrub = [&]() { return ((e - e0) & 1) && min(position() + BN, w.keys()) > w.clear(); };
     if constexpr (!S::F8) {
       // one warp per slot, entries SL apart
       bool landing = false;                           // the slot's last copy is by TMA, and has not been waited for
