@@ -539,8 +539,9 @@ int dg_cache_read(const dg_kv_cache* cache, const dg_kv_batch* batch, int32_t dt
  * included. Products take bf16 operands (an e4m3 row is exact in bf16) with
  * fp32 accumulation; the softmax and its sums are fp32; probabilities are
  * rounded to bf16 for the second product.
- * Errors: DG_EINVAL, DG_ENOMEM (scratch), DG_EUNSUPPORTED (head_dim, batch,
- * row count), DG_ECUDA.
+ * Errors: DG_EINVAL, DG_ENOMEM (scratch), DG_EUNSUPPORTED (head_dim; batch
+ * above 1024; 2^31 cache rows or positions of a page table, or more;
+ * tokens x q_heads above 2^30), DG_ECUDA. Two launches.
  */
 size_t dg_cache_attention_scratch_bytes(const dg_kv_cache* cache, const dg_kv_batch* batch,
                                         int32_t q_heads);

@@ -113,6 +113,16 @@ def test_attention_refusals(lib, kw, code):
     assert dg.dg_last_error(None)
 
 
+def test_more_rows_than_the_kernels_index(lib):
+    b = _batch(tokens=1 << 29)
+    assert _attend(lib, _cache(), b) == dg.DG_EUNSUPPORTED
+    assert lib.dg_cache_attention_scratch_bytes(_cache(), b, 4) == 0 and dg.dg_last_error(None)
+    assert lib.dg_cache_attention_scratch_bytes(_cache(), _batch(), 3) == 0
+    n = lib.dg_cache_attention_scratch_bytes(_cache(), _batch(), 4)
+    assert n > 0 and n % 256 == 0
+    assert _attend(lib, _cache(), _batch(), n=n - 1) == dg.DG_ENOMEM
+
+
 def _norm(lib, **kw):
     a = dict(tokens=3, qh=4, kh=2, D=64, rot=64, inter=0, dtype=dg.DG_BF16, q=P, qts=256, qhs=64, k=P,
              kts=128, khs=64, wq=0, wk=0, off=0.0, eps=1e-6, pos=P, freq=P, qo=P, ko=P)

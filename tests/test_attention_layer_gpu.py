@@ -603,6 +603,26 @@ def test_two_streams_at_once():
             assert same(o, ref[0]) and same(l, ref[1])
 
 
+def test_beside_the_denoise_step():
+    """A denoise block on its own stream while attention calls run on another: both as when alone."""
+    import synthetic
+    w = synthetic.SMALL.replace(C=128, V=4096, d=256, tau=0.5 * 128 * np.log(2), max_steps=4)
+    den = dg.Denoiser(w, synthetic.make_embedding(w).cuda())
+    want, steps = den.block(0)
+    want = want.clone()
+    s = Setup([(3000, 2), (500, 9)], dg.DG_KV_E4M3, 2, 128, 16, seed=3)
+    q = _tokens_q(s, 4)
+    alone = s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL) for _ in range(8)]
+        out, n = den.block(0)
+        torch.cuda.synchronize()
+        assert n == steps and torch.equal(out, want)
+        assert all(same(o, alone[0]) and same(l, alone[1]) for o, l in got)
+    den.close()
+
+
 def test_rows_beyond_four_gigabytes():
     """A cache of over 2^32 bytes (and elements); the sequence lies at its far end."""
     Hk, D, page = 8, 128, 64
