@@ -506,7 +506,7 @@ int dg_cache_write(const dg_kv_cache* cache, const dg_kv_batch* batch, int32_t d
 /*
  * Read the batch's tokens out of the cache: k_out and v_out, contiguous
  * [tokens][kv_heads][head_dim] of dtype (DG_F32 or DG_BF16; both hold every
- * e4m3 row exactly). One launch.
+ * e4m3 row exactly), apart from the cache and from each other. One launch.
  */
 int dg_cache_read(const dg_kv_cache* cache, const dg_kv_batch* batch, int32_t dtype,
                   void* k_out, void* v_out, void* stream);
@@ -531,7 +531,7 @@ int dg_cache_read(const dg_kv_cache* cache, const dg_kv_batch* batch, int32_t dt
  *            mask_words count as zero).
  *   out      bf16 [tokens][q_heads][head_dim], contiguous; a token that sees
  *            nothing gets zeros. lse: float [tokens][q_heads] or NULL
- *            (-infinity where nothing is seen).
+ *            (-infinity where nothing is seen). Neither may overlap an input.
  *   scratch  device, >= dg_cache_attention_scratch_bytes(...) bytes, 256-byte
  *            aligned; holds nothing from one call to the next. Calls that may
  *            overlap on the GPU need one each.

@@ -389,6 +389,47 @@ def test_other_orders_of_the_rows(D):
         s.cache.attend(heads_outer.transpose(1, 2), s.batch, dg.DG_MASK_CAUSAL)
 
 
+@pytest.mark.parametrize("fmt", [dg.DG_KV_BF16, dg.DG_KV_E4M3])
+def test_shared_pages_and_a_page_twice(fmt):
+    """Sequences over one prefix, and a table that names a page twice: the pasts are only read."""
+    s = Setup([(96, 3), (96, 1), (80, 20)], fmt, 2, 128, 16, seed=6)
+    s.table[1, :6] = s.table[0, :6]
+    s.table[2, :3] = s.table[0, 1]
+    q = _tokens_q(s, 4)
+    out, lse = s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL)
+    s.cache.check()
+    _check_attention(s, q, "causal", 128 ** -0.5, out, lse)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_exponents_at_any_address(new):
+    """Exponents that lie at an odd byte are read as the same ones."""
+    s = Setup([(200, new), (33, 2)], dg.DG_KV_E4M3, 2, 128, 16, seed=8)
+    c = s.cache
+    room = [torch.zeros(c.k_exp.numel() + 1, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    odd = [r[1:].view(c.k_exp.shape) for r in room]
+    for o, e in zip(odd, (c.k_exp, c.v_exp)):
+        o.copy_(e)
+    q = _tokens_q(s, 4)
+    out, lse = dg.KVCache(c.k, c.v, *odd).attend(q, s.batch, dg.DG_MASK_CAUSAL)
+    _check_attention(s, q, "causal", 128 ** -0.5, out, lse)
+
+
+@pytest.mark.parametrize("words", [0, 1, 5])
+def test_tree_rows_of_other_widths(words):
+    """Words that are missing count as zero, those beyond the new tokens are not looked at."""
+    s = Setup([(40, 50), (0, 3), (7, 64)], dg.DG_KV_BF16, 2, 64, 16, seed=9)
+    q = _tokens_q(s, 2)
+    bits = np.zeros((s.tokens, max(words, 2)), dtype=np.uint32)
+    bits[:, :2] = _tree(s.new, 4)
+    bits[:, 2:] = 0xFFFFFFFF
+    tree = torch.from_numpy(bits[:, :words].copy().view(np.int32)).cuda()
+    out, lse = s.cache.attend(q, s.batch, dg.DG_MASK_TREE, tree=tree)
+    s.cache.check()
+    bits[:, words:] = 0
+    _check_attention(s, q, "tree", 0.125, out, lse, bits)
+
+
 def test_attention_of_the_largest_batch():
     s = Setup([(b % 37, 1 + (b % 5 == 0)) for b in range(1024)], dg.DG_KV_BF16, 1, 64, 16, seed=1)
     q = _tokens_q(s, 2)

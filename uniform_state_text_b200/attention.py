@@ -4,7 +4,8 @@ paged key/value cache, and attention over it.
 Owners and argument checks only; the work runs in libdg.so (the dg_qk_norm_rope
 and dg_cache_* calls of include/dg.h). Calls run on torch's current stream of
 the tensors' device, allocate their outputs and scratch with torch, and can be
-captured into a CUDA graph.
+captured into a CUDA graph. They are for inference: results carry no gradient.
+A given out or lse shares no memory with an input.
 """
 from __future__ import annotations
 
