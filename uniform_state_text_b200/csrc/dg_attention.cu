@@ -217,7 +217,10 @@ struct Start {
 };
 
 // The whole CTA: tiles per head of every sequence, their prefix sums (in
-// shared memory, pref[batch + 1]), and this CTA's share.
+// shared memory, pref[batch + 1]), and this CTA's share. The sums lie where the
+// first tiles are copied to by TMA: every thread fences its ordinary accesses to
+// them before the last barrier, since a barrier alone does not order those
+// before accesses of the asynchronous proxy.
 template <int ROWS, int BN>
 __device__ __forceinline__ void plan(const Args& a, int64_t* pref, Start* st) {
   const int B = a.w.b.batch;
@@ -291,6 +294,7 @@ __device__ __forceinline__ void plan(const Args& a, int64_t* pref, Start* st) {
       }
     }
   }
+  fence_proxy_async_shared();
   __syncthreads();
 }
 
@@ -408,9 +412,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void fence_async_shared() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 // 16 bytes into shared memory, or zeros where `bytes` is 0.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
@@ -1081,7 +1082,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
         return true;
       }
       load_queries<S>(w, part, smem_u32(smem));
-      fence_async_shared();
+      fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sy.q_full);
       return true;
@@ -1141,7 +1142,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
             copies_landed();
           }
           if (clean) clean_rows<S, BN>(dst, 0, live, scrub, sy);
-          fence_async_shared();
+          fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sy.full[part]);
         }
@@ -1200,7 +1201,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           const bool scrub = to_scrub();
           const int live = live_rows();
           if (scrub || (((e - e0) & 1) && live < r0 + RW)) clean_rows<S, RW>(dst, r0, live, scrub, sy);
-          fence_async_shared();
+          fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&sy.full[slot]);
