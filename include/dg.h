@@ -536,7 +536,10 @@ int dg_cache_read(const dg_kv_cache* cache, const dg_kv_batch* batch, int32_t dt
  *            aligned; holds nothing from one call to the next. Calls that may
  *            overlap on the GPU need one each.
  * What a token does not see does not touch its result, infinities and NaN
- * included. Products take bf16 operands (an e4m3 row is exact in bf16) with
+ * included. Values that it sees and that are not finite add up as numbers do
+ * (times a probability that is zero or rounds to it, an infinity gives NaN or
+ * stays one). A code that its row's exponent takes beyond bf16 (only a caller's
+ * own exponents above 246 do) counts as an infinity. Products take bf16 operands (an e4m3 row is exact in bf16) with
  * fp32 accumulation; the softmax and its sums are fp32; probabilities are
  * rounded to bf16 for the second product.
  * Errors: DG_EINVAL, DG_ENOMEM (scratch), DG_EUNSUPPORTED (head_dim; batch

@@ -1,10 +1,12 @@
 """Attention-layer operators at the edges of their contract: against the fp64 oracle with the
 tolerances of test_attention_layer_gpu.py, and against themselves."""
+import numpy as np
 import pytest
 import torch
 
 import uniform_state_text_b200 as dg
-from test_attention_layer_gpu import MASKS, Setup, _check_attention, _tokens_q
+from oracle import attention as A
+from test_attention_layer_gpu import MASKS, Setup, _check_attention, _tokens_q, _tree, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +37,83 @@ def test_first_tiles_over_the_plan(batch, D, G):
         off += (l.view(torch.int32) != lse.view(torch.int32)).sum()
     assert int(off) == 0
     s.cache.check()
+
+
+# ----------------------------------------------------------------------------- infinite logits
+class Setup16(Setup):
+    """A cache whose rows may lie beyond bf16's range (an exponent above 246 in a caller's own cache):
+    they enter the products as infinities."""
+
+    def values(self, b, n, start, stop):
+        x = super().values(b, n, start, stop)
+        return np.where(np.abs(x) > float(torch.finfo(torch.bfloat16).max), np.copysign(np.inf, x), x)
+
+
+def _infinite(s, name, b, pos, element, sign=1):
+    """An infinity at one element of one row; in e4m3 by the largest code and an exponent of 2^127."""
+    page, place = s.at(b, pos, pos + 1)
+    t = getattr(s.cache, name)
+    if s.fmt == dg.DG_KV_BF16:
+        t[page, :, place, element] = sign * float("inf")
+    else:
+        t.view(torch.uint8)[page, :, place] = 0
+        t.view(torch.uint8)[page, :, place, element] = 0x7E if sign > 0 else 0xFE
+        getattr(s.cache, name + "_exp")[page, :, place] = 254
+
+
+def _check_lse(s, q, mask, scale, lse):
+    """lse is infinite or NaN where the oracle's is, and so."""
+    for b, (p, n) in enumerate(zip(s.past, s.new)):
+        K, V = (s.values(b, x, 0, p + n) for x in "kv")
+        at = s.first[b] + np.arange(n)
+        seen = np.stack([A.seen_by(i, p, n, mask) for i in range(n)])
+        for h in range(q.shape[1]):
+            g = h // (q.shape[1] // s.Hk)
+            want = A.attend(f64(q)[at, h], K[:, g], V[:, g], seen, scale)[1]
+            got = f64(lse)[at, h]
+            bad = ~np.isfinite(want)
+            assert np.array_equal(got[bad], want[bad], equal_nan=True) and np.isfinite(got[~bad]).all(), (b, h)
+
+
+@pytest.mark.parametrize("fmt", [dg.DG_KV_BF16, dg.DG_KV_E4M3])
+@pytest.mark.parametrize("D,G,new", [(128, 2, 3), (256, 2, 70)])
+def test_infinite_logits_at_every_column(fmt, D, G, new):
+    """One infinite element of one past key, at each place of 16 neighbours and in other tiles: rows whose
+    logit is +inf are NaN, those whose logit is -inf have weight 0 there (times an infinite value: NaN)."""
+    for pos in [*range(208, 224), 3, 499]:
+        s = Setup16([(500, new)], fmt, 1, D, 16, seed=D + new)
+        q = _tokens_q(s, G, 5)
+        _infinite(s, "k", 0, pos, 5)
+        _infinite(s, "v", 0, pos, 7)
+        out, lse = s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL)
+        s.cache.check()
+        _check_attention(s, q, "causal", D ** -0.5, out, lse)
+        _check_lse(s, q, "causal", D ** -0.5, lse)
+
+
+# ----------------------------------------------------------------------------- values that are not finite
+@pytest.mark.parametrize("mask", ["causal", "tree"])
+@pytest.mark.parametrize("fmt", [dg.DG_KV_BF16, dg.DG_KV_E4M3])
+@pytest.mark.parametrize("D,G,new,batch", [(64, 2, 20, 1), (128, 8, 30, 1), (128, 2, 140, 1), (256, 2, 70, 1),
+                                           (128, 2, 20, 40), (64, 8, 24, 30), (256, 1, 9, 40)])
+def test_values_that_are_not_finite_meet(fmt, D, G, new, batch, mask):
+    """Infinities and NaN of the past and of new tokens in one column add up as numbers do, in the
+    pieces of several CTAs and within one CTA's share."""
+    s = Setup16([(500, new), (3, new)] * batch, fmt, 2 if batch == 1 else 4, D, 16, seed=D + new)
+    q = _tokens_q(s, G, 5)
+    nan = float("nan")
+    for b, p in enumerate(s.past):
+        for pos, e, sign in ((1, 7, -1), (p + 1, 7, 1), (p + 2, 9, 1), (p + 4, 9, -1), (p + 6, 12, -1), (0, 12, -1),
+                             (p + new - 1, 15, 1)):
+            _infinite(s, "v", b, pos, e, sign)
+        page, place = s.at(b, 2, 3)
+        if fmt == dg.DG_KV_BF16:
+            s.cache.v[page, :, place, 11] = nan
+        else:
+            s.cache.v.view(torch.uint8)[page, :, place, 11] = 0x7F
+        _infinite(s, "v", b, p + 3, 11)
+    words = _tree(s.new, 3, empty=(5,)) if mask == "tree" else None
+    tree = torch.from_numpy(words.view(np.int32)).cuda() if mask == "tree" else None
+    out, lse = s.cache.attend(q, s.batch, MASKS[mask], tree=tree)
+    s.cache.check()
+    _check_attention(s, q, mask, D ** -0.5, out, lse, words)

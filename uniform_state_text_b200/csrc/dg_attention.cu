@@ -515,6 +515,11 @@ __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t pair, float scale) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
   return pack_bf16(f.x * scale, f.y * scale);
 }
+// 2^(e - 127) for a row's exponent byte; any byte is one that fp32 holds, also in
+// rows never written. (A code that it takes beyond bf16 enters as an infinity.)
+__device__ __forceinline__ float exponent_scale(uint8_t e) {
+  return __uint_as_float(max(1u, min(254u, (uint32_t)e)) << 23);
+}
 // kv_row() with the division as a product.
 __device__ __forceinline__ int cache_row(const Args& a, const int32_t* table, int64_t pos, int head) {
   const dg_kv_cache& c = a.w.c;
@@ -688,11 +693,11 @@ __device__ __forceinline__ void convert(const uint8_t* exps, int r0, uint32_t sr
   for (int n = 0; n < N; n += K) {
     const int r = r0 + n * RPI + lane / CPR;
     uint4 v[K];
-    float scale[K];                                  // any byte is an exponent, also in rows never written
+    float scale[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       v[k] = ld_shared(src + (r + k * RPI) * S::DP + q * 16);
-      scale[k] = __uint_as_float(max(1u, min(254u, (uint32_t)exps[r + k * RPI])) << 23);
+      scale[k] = exponent_scale(exps[r + k * RPI]);
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -745,14 +750,34 @@ __device__ __forceinline__ void clean_rows(uint32_t slot, int r0, int live, bool
   if (dirty) *(volatile int*)&sy.nonfinite = 1;
 }
 
-// o (columns d .. d + 3 of a row's sum) with the infinities and NaN among the
-// values that new token i of the sequence sees in the segment's keys from
-// position `from` on, where clean_rows has left them out. They decide the result
-// wherever there are any.
+// Logit of a query row (head_dim bf16) and a cache row, as the products have it up
+// to the order of its sum. For rows whose value is not finite only.
+template <class S>
+__device__ __forceinline__ float logit_of(const Args& a, const __nv_bfloat16* q, int row) {
+  float z = 0.f;
+  for (int d = 0; d < a.w.c.head_dim; ++d) {
+    const int64_t at = (int64_t)row * a.w.c.head_dim + d;
+    uint32_t k;
+    if constexpr (S::F8)
+      k = codes_to_bf16(static_cast<const uint8_t*>(a.w.c.k)[at], exponent_scale(a.w.c.k_exp[row]));
+    else
+      k = static_cast<const uint16_t*>(a.w.c.k)[at];
+    z = fmaf(to_f32(q[d]), __uint_as_float(k << 16), z);
+  }
+  return z * a.scale_log2;
+}
+
+// o (columns d .. d + 3 of the sum of output row `orow`, one of the sequence's) and
+// the infinities and NaN among the values that it sees in the segment's keys from
+// position `from` on, where clean_rows has left them out. They are added as they
+// are, whatever their positive weight; times a weight of zero (a logit of minus
+// infinity) an infinity is NaN.
 template <class S, typename W>
-__device__ __noinline__ float4 with_not_finite(const W w, const uint32_t* tree, int i, int d, int64_t from, float4 o) {
+__device__ __noinline__ float4 with_not_finite(const W w, const uint32_t* tree, int orow, int d, int64_t from, float4 o) {
   const Args& a = w.a;
   if (d >= a.w.c.head_dim) return o;
+  const int token = orow / a.q_heads, i = token - w.t0;
+  const __nv_bfloat16* q = a.q + (int64_t)token * a.q_ts + (int64_t)(orow - token * a.q_heads) * a.q_hs;
   float x[4] = {0.f, 0.f, 0.f, 0.f};
   const int64_t end = min(w.keys(), (int64_t)w.te * S::BN);
   for (int64_t j = max(from, (int64_t)w.tb * S::BN); j < end; ++j) {
@@ -760,21 +785,24 @@ __device__ __noinline__ float4 with_not_finite(const W w, const uint32_t* tree, 
     const int row = cache_row(a, a.w.b.page_table + (int64_t)w.b * a.w.b.table_stride, j, w.h);
     if (row < 0) continue;
     const int64_t at = (int64_t)row * a.w.c.head_dim + d;
+    uint2 c;                                         // the four values as they enter the products
     if constexpr (S::F8) {
-      const uint32_t c = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.w.c.v) + at);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) if ((c >> (8 * k) & 0x7f) == 0x7f) x[k] = NAN;
+      const uint32_t codes = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.w.c.v) + at);
+      const float scale = exponent_scale(a.w.c.v_exp[row]);
+      c = make_uint2(codes_to_bf16(codes, scale), codes_to_bf16(codes >> 16, scale));
     } else {
-      const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.w.c.v) + at);
+      c = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.w.c.v) + at);
+    }
+    if (only_finite(c.x) == c.x && only_finite(c.y) == c.y) continue;
+    const bool zero = logit_of<S>(a, q, row) == -INFINITY;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t half = (k < 2 ? c.x : c.y) >> (16 * (k & 1)) & 0xffffu;
-        if (!finite_bf16(half)) x[k] += __uint_as_float(half << 16);
-      }
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t half = (k < 2 ? c.x : c.y) >> (16 * (k & 1)) & 0xffffu;
+      if (!finite_bf16(half)) x[k] += zero ? NAN : __uint_as_float(half << 16);
     }
   }
-  return make_float4(x[0] == 0.f ? o.x : x[0], x[1] == 0.f ? o.y : x[1], x[2] == 0.f ? o.z : x[2],
-                     x[3] == 0.f ? o.w : x[3]);
+  return make_float4(x[0] == 0.f ? o.x : o.x + x[0], x[1] == 0.f ? o.y : o.y + x[1],
+                     x[2] == 0.f ? o.z : o.z + x[2], x[3] == 0.f ? o.w : o.w + x[3]);
 }
 
 // A 4 x 4 transposition of 16-byte pieces over each four lanes: lane q of four
@@ -1012,7 +1040,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           if (fix && valid) {
 #pragma unroll
             for (int d = 0; d < 32; d += 4) {
-              const float4 u = with_not_finite<S>(w, tree, i, c * 32 + d, w.clear() / BN * BN,
+              const float4 u = with_not_finite<S>(w, tree, orow, c * 32 + d, w.clear() / BN * BN,
                                                   make_float4(o[d], o[d + 1], o[d + 2], o[d + 3]));
               o[d] = u.x; o[d + 1] = u.y; o[d + 2] = u.z; o[d + 3] = u.w;
             }
