@@ -539,7 +539,9 @@ int dg_cache_read(const dg_kv_cache* cache, const dg_kv_batch* batch, int32_t dt
  * included. Values that it sees and that are not finite add up as numbers do
  * (times a probability that is zero or rounds to it, an infinity gives NaN or
  * stays one). A code that its row's exponent takes beyond bf16 (only a caller's
- * own exponents above 246 do) counts as an infinity. Products take bf16 operands (an e4m3 row is exact in bf16) with
+ * own exponents above 246 do) counts as an infinity. Products q.k are held in
+ * fp32, one beyond it counts as infinite: +infinity or NaN makes the row NaN,
+ * -infinity weighs nothing. Products take bf16 operands (an e4m3 row is exact in bf16) with
  * fp32 accumulation; the softmax and its sums are fp32; probabilities are
  * rounded to bf16 for the second product.
  * Errors: DG_EINVAL, DG_ENOMEM (scratch), DG_EUNSUPPORTED (head_dim; batch

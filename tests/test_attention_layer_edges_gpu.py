@@ -67,7 +67,7 @@ def _check_lse(s, q, mask, scale, lse):
         K, V = (s.values(b, x, 0, p + n) for x in "kv")
         at = s.first[b] + np.arange(n)
         seen = np.stack([A.seen_by(i, p, n, mask) for i in range(n)])
-        for h in range(q.shape[1]):
+        for h in range(0, q.shape[1], 3):
             g = h // (q.shape[1] // s.Hk)
             want = A.attend(f64(q)[at, h], K[:, g], V[:, g], seen, scale)[1]
             got = f64(lse)[at, h]
@@ -76,7 +76,7 @@ def _check_lse(s, q, mask, scale, lse):
 
 
 @pytest.mark.parametrize("fmt", [dg.DG_KV_BF16, dg.DG_KV_E4M3])
-@pytest.mark.parametrize("D,G,new", [(128, 2, 3), (256, 2, 70)])
+@pytest.mark.parametrize("D,G,new", [(64, 8, 30), (128, 8, 30), (128, 2, 3), (256, 2, 70)])
 def test_infinite_logits_at_every_column(fmt, D, G, new):
     """One infinite element of one past key, at each place of 16 neighbours and in other tiles: rows whose
     logit is +inf are NaN, those whose logit is -inf have weight 0 there (times an infinite value: NaN)."""
@@ -89,6 +89,35 @@ def test_infinite_logits_at_every_column(fmt, D, G, new):
         s.cache.check()
         _check_attention(s, q, "causal", D ** -0.5, out, lse)
         _check_lse(s, q, "causal", D ** -0.5, lse)
+
+
+@pytest.mark.parametrize("D,G,new", [(64, 8, 30), (128, 8, 20), (128, 2, 3), (256, 2, 9)])
+def test_infinite_logits_within_one_share(D, G, new):
+    """Many sequences, so that one CTA goes through the tiles before and behind the infinite one."""
+    s = Setup([(300, new)] * 60, dg.DG_KV_BF16, 4, D, 16, seed=D + new)
+    q = _tokens_q(s, G, 5)
+    for b in range(60):
+        _infinite(s, "k", b, (b * 37) % (300 + new), 5)
+    out, lse = s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL)
+    s.cache.check()
+    _check_attention(s, q, "causal", D ** -0.5, out, lse)
+    _check_lse(s, q, "causal", D ** -0.5, lse)
+
+
+@pytest.mark.parametrize("mask", ["causal", "full"])
+@pytest.mark.parametrize("D,G,new,batch", [(64, 8, 40, 1), (128, 8, 30, 1), (128, 2, 3, 1), (256, 2, 70, 1),
+                                           (64, 8, 40, 60), (128, 8, 30, 60), (128, 2, 3, 60)])
+def test_rows_whose_logits_are_all_minus_infinity(D, G, new, batch, mask):
+    """They weigh nothing, like rows that see nothing; and a row of +inf and finite logits is NaN."""
+    s = Setup([(500, new)] * batch, dg.DG_KV_BF16, 1, D, 16, seed=D)
+    q = _tokens_q(s, G, 5)
+    s.cache.k[..., 5] = -float("inf")
+    out, lse = s.cache.attend(q, s.batch, MASKS[mask])
+    s.cache.check()
+    _check_attention(s, q, mask, D ** -0.5, out, lse)
+    down = q[..., 5] > 0
+    assert not out[down].any() and (lse[down] == -float("inf")).all()
+    assert out[~down].isnan().all() and lse[~down].isnan().all()
 
 
 # ----------------------------------------------------------------------------- values that are not finite

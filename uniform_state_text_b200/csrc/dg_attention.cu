@@ -455,11 +455,12 @@ __device__ __forceinline__ uint64_t exp2_mufu2(uint64_t x) { return pack2(ex2(lo
 // 2^x without the special-function unit, of which an SM has 16 lanes to 128 for
 // arithmetic: x = n + f with n the nearest whole number (by adding 1.5 2^23),
 // 2^f on [-1/2, 1/2] by the polynomial of degree 5 through 2^f at the Chebyshev
-// points (relative error 2.1e-7 in fp32), n added to the exponent. For x from
-// -126 (smaller ones give 2^-126) to 127, not NaN.
+// points (relative error 2.1e-7 in fp32), n added to the exponent. For x up to
+// 127, not NaN; below -126.5 the result is a denormal number, and below -127, minus
+// infinity included, 2^-149, which is zero in bf16.
 __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x) {
   constexpr float kMagic = 12582912.0f;
-  x = pack2(fmaxf(lo2(x), -126.0f), fmaxf(hi2(x), -126.0f));
+  x = pack2(fmaxf(lo2(x), -127.0f), fmaxf(hi2(x), -127.0f));
   const uint64_t r = add2(x, pack2(kMagic, kMagic));
   const uint64_t f = fma2(add2(r, pack2(-kMagic, -kMagic)), pack2(-1.f, -1.f), x);
   uint64_t p = pack2(0.00133908633f, 0.00133908633f);
@@ -925,7 +926,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
               }
               top = max3_nan(u0, u1, u1);
             }
-            plain = !__any_sync(0xffffffffu, top != top && valid);    // NaN: below, where it goes by MUFU
+            // a maximum that is NaN or (scaled) infinite: below, where all goes by MUFU
+            plain = !__any_sync(0xffffffffu, valid && !(fabsf(top * a.scale_log2) < INFINITY));
           }
           // others: 32 columns at a time
           const int chunks = plain ? 0 : BN / 32;
