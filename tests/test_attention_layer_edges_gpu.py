@@ -6,7 +6,7 @@ import torch
 
 import uniform_state_text_b200 as dg
 from oracle import attention as A
-from test_attention_layer_gpu import MASKS, Setup, _check_attention, _tokens_q, _tree, f64
+from test_attention_layer_gpu import MASKS, U32, Setup, _check_attention, _tokens_q, _tree, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -118,6 +118,59 @@ def test_rows_whose_logits_are_all_minus_infinity(D, G, new, batch, mask):
     down = q[..., 5] > 0
     assert not out[down].any() and (lse[down] == -float("inf")).all()
     assert out[~down].isnan().all() and lse[~down].isnan().all()
+
+
+@pytest.mark.parametrize("batch", [1, 40])
+@pytest.mark.parametrize("G,new", [(8, 30), (2, 3)])
+def test_logits_beyond_fp32(G, new, batch):
+    """q.k beyond fp32 counts as infinite; a finite q.k whose scaled logit lies beyond fp32, or is too
+    large for its fraction to be held, still gets the softmax's weights."""
+    s = Setup([(500, new)] * batch, dg.DG_KV_BF16, 1, 64, 16, seed=3)
+    q = torch.ones_like(_tokens_q(s, G, 5))
+    for big, qs, scale in ((2.0 ** 100, 2.0 ** 40, 1.0), (2.0 ** 115, 1.0, 2.0 ** 10)):
+        for sign in (1, -1):
+            for b in range(batch):
+                page, place = s.at(b, 215, 216)
+                s.cache.k[page, :, place] = sign * big
+            out, lse = s.cache.attend(q * qs, s.batch, dg.DG_MASK_FULL, scale=scale)
+            s.cache.check()
+            if sign > 0 and scale == 1.0:
+                assert out.isnan().all() and lse.isnan().all()
+                continue
+            # where one key is ahead by far it has all the weight
+            for b in range(batch):
+                K, V = (s.values(b, x, 0, 500 + new)[:, 0] for x in "kv")
+                z = K.sum(1) * qs * scale
+                top = int(z.argmax())
+                rows = slice(int(s.first[b]), int(s.first[b + 1]))
+                err = np.abs(f64(out[rows]) - V[top]).max() if np.sort(z)[-2] < z[top] - 1000 else 0.0
+                assert err == 0.0, (b, err)
+                assert not out[rows].isnan().any()
+                got, want = f64(lse[rows]), z[top] + np.log(np.exp(z - z[top]).sum())
+                delta = (64 * 2.0 ** -23 + 4 * U32) * (np.abs(K).sum(1) * qs * scale).max()   # of a logit, as there
+                assert (np.isposinf(got) if want > 3.5e38 else np.abs(got - want) <= delta + 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("step", [0.0, 0.5])
+@pytest.mark.parametrize("size", [1e5, 3e7, 1e9, 1e20])
+@pytest.mark.parametrize("G,new,batch", [(8, 30, 1), (8, 30, 30), (2, 3, 1), (2, 3, 60)])
+def test_large_logits(G, new, batch, size, step):
+    """Rows whose logits are all near one large number: the values' mean where they are equal, the weights
+    of their differences where those are held; and never NaN."""
+    s = Setup([(500, new)] * batch, dg.DG_KV_BF16, 1, 64, 16, seed=3)
+    s.cache.k.zero_()
+    s.cache.k[..., 0] = 1.0
+    s.cache.k[..., 1] = step * torch.randint(0, 3, s.cache.k.shape[:3], generator=s.g, device="cuda")
+    for sign in (1, -1):
+        q = torch.zeros_like(_tokens_q(s, G, 5))
+        q[..., 0] = sign * size
+        q[..., 1] = torch.randn(q.shape[:2], generator=s.g, device="cuda")
+        scale = 1.0 if size < 1e6 else 0.25
+        out, lse = s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL, scale=scale)
+        s.cache.check()
+        assert out.float().isfinite().all() and lse.isfinite().all()
+        if step == 0.0 or size < 1e6:
+            _check_attention(s, q, "causal", scale, out, lse)
 
 
 # ----------------------------------------------------------------------------- values that are not finite

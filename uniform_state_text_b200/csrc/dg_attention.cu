@@ -4,7 +4,9 @@
 // For one query row, over the keys j it sees, with t_j = scale log2(e) q.k_j:
 //   m = max t_j,  l = sum 2^(t_j - m),  out = sum 2^(t_j - m) v_j / l,
 //   lse = (m + log2 l) ln 2
-// in one pass over the keys: a larger maximum rescales l and the running sum.
+// in one pass over the keys: a larger maximum rescales l and the running sum. (m
+// is kept before the scale, where it is one of the logits to the bit, so that
+// differences from it stay differences however large the logits are.)
 //
 // Rows. The query heads of one key/value head and the tokens of one sequence
 // are packed into one matrix, row r = token r / G, head r % G (G query heads
@@ -83,6 +85,7 @@ constexpr int kMaxCtas = 148;                 // scratch is laid out for at most
 constexpr int TMEM_COLS = 512;
 constexpr int kItem = 3;                      // an item's cost beside its key tiles, in key tiles
 constexpr float kGrow = 8.0f;                 // log2 growth of a maximum that rescales O
+constexpr float kLarge = 16777216.0f;         // scaled logits of this size have steps of one and more
 constexpr unsigned long long kWaitNs = 2000000000ull;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -103,7 +106,7 @@ struct Args {
   float* lse;
   // scratch
   float* part_o;               // [CTAs][2][rows][DP] unnormalised sums
-  float2* part_ml;             // [CTAs][2][rows] their m (log2 units) and l
+  float2* part_ml;             // [CTAs][2][rows] their m (unscaled) and l
   struct Open* open;           // [CTAs] the item a CTA begins and does not finish
   int rows;                    // rows kept per piece
   int box;                     // rows per TMA copy: a power of two that divides page_size; 0: no TMA
@@ -896,7 +899,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       const uint32_t* tree = a.mask == DG_MASK_TREE ? a.tree + (int64_t)(w.t0 + i) * a.words : nullptr;
       // tiles that reach beyond this position hold some that the row may not see
       const int64_t clear = a.mask == DG_MASK_FULL ? w.keys() : a.mask == DG_MASK_CAUSAL ? (int64_t)w.past + i + 1 : w.past;
-      float m = -INFINITY, l = 0.f;                   // m in log2 units
+      float m = -INFINITY, l = 0.f;                   // m unscaled
       for (int t = w.tb; t < w.te; ++t, ++gt) {
         const int bar = 4 * x + (int)(gt & 3);
         if (!wait_warp(&sy.s_full[bar], (gt >> 2) & 1, sy, a)) { ok = false; break; }
@@ -926,8 +929,9 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
               }
               top = max3_nan(u0, u1, u1);
             }
-            // a maximum that is NaN or (scaled) infinite: below, where all goes by MUFU
-            plain = !__any_sync(0xffffffffu, valid && !(fabsf(top * a.scale_log2) < INFINITY));
+            // a maximum that is NaN, infinite or very large: below, with differences of
+            // unscaled logits (here the maximum's rounding would be one of the exponent)
+            plain = !__any_sync(0xffffffffu, valid && !(fabsf(top * a.scale_log2) < kLarge));
           }
           // others: 32 columns at a time
           const int chunks = plain ? 0 : BN / 32;
@@ -949,14 +953,14 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
             }
             top = fmaxf(top, fmaxf(u0, u1));
           }
-          top *= a.scale_log2;
           // the maximum in use moves at the first tile and when it has grown by kGrow
+          // (two of -infinity: NaN, no move)
           const bool first = t == w.tb;
-          const bool move = top > m + kGrow || (m == -INFINITY && top > m);
+          const bool move = (top - m) * a.scale_log2 > kGrow;
           if (!first && __any_sync(0xffffffffu, move && valid)) {
             if (!pv_done(gt - 1)) { ok = false; break; }
             tc_fence_after();
-            const float f = move ? ex2(m - top) : 1.f;
+            const float f = move ? ex2((m - top) * a.scale_log2) : 1.f;
             l *= f;
 #pragma unroll 1
             for (int c = 0; c < S::DP / 32; ++c) {
@@ -974,7 +978,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           const float sub = m == -INFINITY ? 0.f : m;  // a row that has seen nothing yet: P = 0
           float l0 = 0.f, l1 = 0.f;
           if (plain) {
-            const uint64_t sc = pack2(a.scale_log2, a.scale_log2), ns = pack2(-sub, -sub);
+            const float to = -sub * a.scale_log2;
+            const uint64_t sc = pack2(a.scale_log2, a.scale_log2), ns = pack2(to, to);
             uint64_t ls = pack2(0.f, 0.f);
             tmem_ld16_issue(t_s, ra);
 #pragma unroll
@@ -1006,8 +1011,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
             uint32_t p[16];
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
-              const float e0 = ex2(fmaf(s[j], a.scale_log2, -sub));
-              const float e1 = ex2(fmaf(s[j + 1], a.scale_log2, -sub));
+              const float e0 = ex2((s[j] - sub) * a.scale_log2);
+              const float e1 = ex2((s[j + 1] - sub) * a.scale_log2);
               l0 += e0;
               l1 += e1;
               p[j >> 1] = pack_bf16(e0, e1);
@@ -1079,7 +1084,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
             }
           }
         }
-        if (valid && whole && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        if (valid && whole && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : fmaf(m, a.scale_log2, log2f(l)) * kLn2;
         if (valid && !whole) a.part_ml[prow] = make_float2(m, l);
       }
       __syncwarp();
@@ -1386,7 +1391,7 @@ __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Args a, in
     float m = ml.x;
 #pragma unroll
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float f = ex2(ml.x - (m == -INFINITY ? 0.f : m));
+    const float f = ex2((ml.x - (m == -INFINITY ? 0.f : m)) * a.scale_log2);
     float l = lane < n ? f * ml.y : 0.f;
 #pragma unroll
     for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
@@ -1417,7 +1422,7 @@ __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Args a, in
 #pragma unroll
         for (int k = 0; k < V; ++k) o[k] = 0.f;
         for (int p = 0; p < 8; ++p) {
-          const float g = ex2(m_s[p] - base);
+          const float g = ex2((m_s[p] - base) * a.scale_log2);
           l += g * l_s[p];
 #pragma unroll
           for (int k = 0; k < V; ++k) o[k] = fmaf(o_s[p][lane * V + k], g, o[k]);
@@ -1435,7 +1440,7 @@ __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Args a, in
     for (int k = 0; k < V; k += 2)
       if (lane * V + k < a.w.c.head_dim)
         *reinterpret_cast<uint32_t*>(a.out + orow * a.w.c.head_dim + lane * V + k) = pack_bf16(o[k] * inv, o[k + 1] * inv);
-    if (lane == 0 && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    if (lane == 0 && a.lse) a.lse[orow] = l == 0.f ? -INFINITY : fmaf(m, a.scale_log2, log2f(l)) * kLn2;
   }
 }
 
