@@ -199,3 +199,42 @@ def test_values_that_are_not_finite_meet(fmt, D, G, new, batch, mask):
     out, lse = s.cache.attend(q, s.batch, MASKS[mask], tree=tree)
     s.cache.check()
     _check_attention(s, q, mask, D ** -0.5, out, lse, words)
+
+
+# ----------------------------------------------------------------------------- the rotation's angle
+def _turns(pos, freq):
+    """pos freq / 2 pi mod 1 from whole numbers: pi by Machin's formula to 300 bits."""
+    one = 1 << 300
+
+    def arctan_inverse(n):
+        total, term, k = 0, one // n, 0
+        while term:
+            total += term // (2 * k + 1) * (1 - 2 * (k & 1))
+            term //= n * n
+            k += 1
+        return total
+
+    pi = 4 * (4 * arctan_inverse(5) - arctan_inverse(239))
+    top, bottom = float(freq).as_integer_ratio()
+    return (int(pos) * top * one * one // (bottom * 2 * pi) % one) / one
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_angles_at_far_positions(sign, interleaved):
+    """Every angle is right to 2^-25 turns, for frequencies of either sign up to 1000. A pair (1, 0) comes
+    out as one number times (cos t, sin t); sine, cosine and product add 3 u32 to the angle, in radians
+    (2 u32 of the function and u32 of the product, relative, on either)."""
+    r = np.random.default_rng(5)
+    freq = sign * np.concatenate([10.0 ** r.uniform(-6, 2.99, 96), r.uniform(0, 2 * np.pi, 30), [0.0, 999.9]])
+    pos = [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1234567, -2 ** 30 - 1, 1, -1, 0, 131071]
+    x = torch.zeros(len(pos), 1, 256, device="cuda")
+    first, second = (slice(0, None, 2), slice(1, None, 2)) if interleaved else (slice(0, 128), slice(128, 256))
+    x[..., first] = 1.0
+    y, _ = dg.qk_norm_rope(x, x[:, :0], None, None, torch.tensor(pos, dtype=torch.int32, device="cuda"),
+                           torch.from_numpy(freq).cuda(), interleaved=interleaved, eps=0.0)
+    y = f64(y)[:, 0]
+    got = np.arctan2(y[:, second], y[:, first]) / (2 * np.pi)
+    want = np.array([[_turns(p, f) for f in freq] for p in pos])
+    err = np.abs((got - want + 0.5) % 1 - 0.5)
+    assert err.max() <= 2.0 ** -25 + 3 * U32 / (2 * np.pi), err.max() * 2 ** 25

@@ -93,12 +93,16 @@ struct NormArgs {
 // product with an integer position, mod 2^64, is the phase itself, with no
 // range reduction. 1 / (2 pi) is taken in two doubles and the product's
 // rounding is kept, so that the fraction is right to 2^-63 turns and the phase
-// to 2^-32 turns at any int32 position.
+// to 2^-32 turns at any int32 position. (Of the magnitude: hi - floor(hi) is
+// exact for hi >= 0, but would round for a small negative one. The sign is then
+// exact mod 2^64.)
 __device__ __forceinline__ uint64_t turns_per_position(double radians) {
-  const double hi = radians * 0.15915494309189535;
-  const double lo = fma(radians, 0.15915494309189535, -hi) + radians * -9.839338337591243e-18;
+  const double r = fabs(radians);
+  const double hi = r * 0.15915494309189535;
+  const double lo = fma(r, 0.15915494309189535, -hi) + r * -9.839338337591243e-18;
   const double t = hi - floor(hi);
-  return (uint64_t)(t * 18446744073709551616.0) + (uint64_t)(int64_t)(lo * 18446744073709551616.0);
+  const uint64_t turns = (uint64_t)(t * 18446744073709551616.0) + (uint64_t)(int64_t)(lo * 18446744073709551616.0);
+  return radians < 0.0 ? 0 - turns : turns;
 }
 __device__ __forceinline__ void sincos_turns(uint64_t phase, float* s, float* c) {
   // the top 32 bits, signed, as multiples of pi in [-1, 1); the rounding to
