@@ -238,3 +238,17 @@ def test_angles_at_far_positions(sign, interleaved):
     want = np.array([[_turns(p, f) for f in freq] for p in pos])
     err = np.abs((got - want + 0.5) % 1 - 0.5)
     assert err.max() <= 2.0 ** -25 + 3 * U32 / (2 * np.pi), err.max() * 2 ** 25
+
+
+# ----------------------------------------------------------------------------- the owners
+def test_a_refused_batch_leaves_no_size_behind():
+    """A batch that the library refuses, then a right one of the same tokens, sequences and heads."""
+    s = Setup([(40, 3)], dg.DG_KV_BF16, 1, 64, 1024, seed=1)
+    q = _tokens_q(s, 2)
+    wide = torch.zeros(1, 1 << 21, dtype=torch.int32, device="cuda")       # 2^31 positions
+    bad = dg.KVBatch(wide, s.batch.first, s.batch.past, s.tokens)
+    with pytest.raises(dg.DgError) as e:
+        s.cache.attend(q, bad, dg.DG_MASK_CAUSAL)
+    assert e.value.code == dg.DG_EUNSUPPORTED
+    out, lse = s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL)
+    _check_attention(s, q, "causal", 0.125, out, lse)

@@ -224,7 +224,9 @@ class KVCache:
         key = (tokens, batch.c.batch, hq)
         n = self._scratch.get(key)
         if n is None:
-            n = self._scratch[key] = dg_cache_attention_scratch_bytes(c, batch.c, hq)
+            n = dg_cache_attention_scratch_bytes(c, batch.c, hq)
+            if n:                           # 0: the call below is refused, for reasons the key lacks
+                self._scratch[key] = n
         scratch = self.status.new_empty((n // 4,))
         _call(index, dg_cache_attention, c, batch.c, hq, q.data_ptr(), *qs,
               c.head_dim ** -0.5 if scale is None else scale, mask, tree_ptr, words, out.data_ptr(),
