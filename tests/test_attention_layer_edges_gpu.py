@@ -252,3 +252,12 @@ def test_a_refused_batch_leaves_no_size_behind():
     assert e.value.code == dg.DG_EUNSUPPORTED
     out, lse = s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL)
     _check_attention(s, q, "causal", 0.125, out, lse)
+
+
+def test_sizes_kept_for_many_token_counts_are_bounded():
+    s = Setup([(5, 600)], dg.DG_KV_BF16, 1, 64, 16, seed=1)
+    q = _tokens_q(s, 1)
+    for n in range(1, 600):
+        s.cache.attend(q[:n], dg.KVBatch(s.table, s.batch.first.clamp(max=n), s.batch.past, n), dg.DG_MASK_CAUSAL)
+    s.cache.check()
+    assert len(s.cache._scratch) <= 64

@@ -21,6 +21,7 @@ from . import (DG_BF16, DG_F32, DG_KV_BF16, DG_KV_E4M3, DG_MASK_CAUSAL, DG_MASK_
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch.cuda.current_device
 _empty_like, _contiguous = torch.empty_like, torch.contiguous_format
+_KEPT_SIZES = 64            # scratch sizes a cache remembers (one per shape of call)
 _DTYPES = {torch.bfloat16: DG_BF16, torch.float32: DG_F32}
 
 
@@ -226,6 +227,8 @@ class KVCache:
         if n is None:
             n = dg_cache_attention_scratch_bytes(c, batch.c, hq)
             if n:                           # 0: the call below is refused, for reasons the key lacks
+                if len(self._scratch) == _KEPT_SIZES:
+                    self._scratch.clear()
                 self._scratch[key] = n
         scratch = self.status.new_empty((n // 4,))
         _call(index, dg_cache_attention, c, batch.c, hq, q.data_ptr(), *qs,
