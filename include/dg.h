@@ -555,6 +555,21 @@ int dg_cache_attention(const dg_kv_cache* cache, const dg_kv_batch* batch, int32
                        int32_t mask, const uint32_t* tree_mask, int32_t mask_words,
                        void* out, float* lse, void* scratch, size_t scratch_bytes, void* stream);
 
+/*
+ * Failure-path testing of dg_cache_attention's bounded waits, as
+ * dg_inject_stall is for a context's. A wait that runs out raises DG_ETIMEOUT in
+ * the cache's status word; every thread block then lets its copies and products
+ * in flight finish and returns, and the call's outputs are not to be used.
+ *   wait_limit_ns  the limit of every wait (0: the default, 2 s).
+ *   stall          0 for normal operation; n > 0 withholds one hand-over between
+ *                  the warps of each thread block, at its n-th key tile, so that
+ *                  the waits behind it run out.
+ * For the whole process, host only; later calls take it (a captured graph keeps
+ * what it was captured with). Errors: DG_EINVAL (limit outside [0, 60 s],
+ * stall < 0).
+ */
+int dg_cache_attention_inject_stall(int64_t wait_limit_ns, int32_t stall);
+
 /* Release the context (host memory and graph objects only). */
 int dg_free(dg_ctx* ctx);
 

@@ -261,3 +261,36 @@ def test_sizes_kept_for_many_token_counts_are_bounded():
         s.cache.attend(q[:n], dg.KVBatch(s.table, s.batch.first.clamp(max=n), s.batch.past, n), dg.DG_MASK_CAUSAL)
     s.cache.check()
     assert len(s.cache._scratch) <= 64
+
+
+# ----------------------------------------------------------------------------- waits that run out
+@pytest.mark.parametrize("fmt,D,G,page,new", [
+    (dg.DG_KV_BF16, 128, 2, 64, 1), (dg.DG_KV_BF16, 128, 8, 64, 33), (dg.DG_KV_E4M3, 128, 2, 64, 1),
+    (dg.DG_KV_E4M3, 64, 8, 64, 33), (dg.DG_KV_E4M3, 256, 2, 32, 4), (dg.DG_KV_BF16, 256, 3, 16, 5),
+    (dg.DG_KV_BF16, 64, 3, 5, 70), (dg.DG_KV_E4M3, 48, 40, 5, 2)])      # single rows; queries row by row
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(fmt, D, G, page, new):
+    """One hand-over withheld at a CTA's first, third or tenth key tile, limit 20 ms: the call returns with
+    DG_ETIMEOUT in the status word, copies drained, and the next call is as before to the bit."""
+    s = Setup([(3000 - 61 * b, new) for b in range(20)], fmt, 4, D, page, seed=D)
+    q = _tokens_q(s, G, 2)
+    want, lse = s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL)
+    s.cache.check()
+    try:
+        for tile in (1, 3, 10):
+            dg.dg_cache_attention_inject_stall(20_000_000, tile)
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL)
+            end.record()
+            with pytest.raises(dg.DgError) as e:
+                s.cache.check()
+            assert e.value.code == dg.DG_ETIMEOUT
+            assert 15 < start.elapsed_time(end) < 500            # ms; well under the default 2 s
+            dg.dg_cache_attention_inject_stall(0, 0)
+            s.cache.status.zero_()
+            out, l = s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL)
+            s.cache.check()
+            assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+            assert torch.equal(l.view(torch.int32), lse.view(torch.int32))
+    finally:
+        dg.dg_cache_attention_inject_stall(0, 0)

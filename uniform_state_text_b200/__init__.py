@@ -117,6 +117,7 @@ def lib():
     L.dg_cache_attention_scratch_bytes.restype = ctypes.c_size_t
     L.dg_cache_attention.argtypes = kvp + [_I, _P, i64, i64, f32, _I, _P, _I, _P, _P, _P,
                                            ctypes.c_size_t, _P]
+    L.dg_cache_attention_inject_stall.argtypes = [i64, _I]
     L.dg_free.argtypes = [_P]
     L.dg_last_error.argtypes = [_P]
     L.dg_last_error.restype = ctypes.c_char_p
@@ -125,7 +126,7 @@ def lib():
                  "dg_impl", "dg_free", "dg_vocab_attention_static", "dg_denoise_step_partial",
                  "dg_denoise_step_finish", "dg_tc_schedule", "dg_inject_stall",
                  "dg_self_condition", "dg_qk_norm_rope", "dg_cache_write", "dg_cache_read",
-                 "dg_cache_attention"):
+                 "dg_cache_attention", "dg_cache_attention_inject_stall"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -297,6 +298,11 @@ def dg_cache_attention(cache: dg_kv_cache, batch: dg_kv_batch, q_heads: int, q_p
                                     q_token_stride, q_head_stride, scale, mask, tree_mask_ptr,
                                     mask_words, out_ptr, lse_ptr, scratch_ptr, scratch_bytes,
                                     stream_ptr), None)
+
+
+def dg_cache_attention_inject_stall(wait_limit_ns: int, stall: int) -> None:
+    """Failure-path testing: limit every wait of later attention calls and withhold one hand-over."""
+    _check(lib().dg_cache_attention_inject_stall(int(wait_limit_ns), int(stall)), None)
 
 
 def dg_inject_stall(ctx, wait_limit_ns: int, stall: int) -> None:

@@ -86,7 +86,7 @@ constexpr int TMEM_COLS = 512;
 constexpr int kItem = 3;                      // an item's cost beside its key tiles, in key tiles
 constexpr float kGrow = 8.0f;                 // log2 growth of a maximum that rescales O
 constexpr float kLarge = 16777216.0f;         // scaled logits of this size have steps of one and more
-constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr unsigned long long kWaitNs = 2000000000ull;   // a wait's limit by default
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct Args {
@@ -111,6 +111,9 @@ struct Args {
   int rows;                    // rows kept per piece
   int box;                     // rows per TMA copy: a power of two that divides page_size; 0: no TMA
   int q_box;                   // queries by TMA, 32 rows (32 / G tokens of G heads) at a time
+  // failure-path testing
+  unsigned long long wait_ns;  // the limit of every wait
+  uint32_t stall;              // > 0: the softmax does not announce each CTA's key tile of this number, from 1
 
   __device__ __forceinline__ uint32_t over_g(uint32_t r) const {
     return (uint32_t)(((uint64_t)r * g_mul) >> g_shift);
@@ -334,15 +337,15 @@ struct Sync {
 };
 
 // Bounded wait on an mbarrier phase; gives up on the CTA's abort flag or after
-// kWaitNs (then raises DG_ETIMEOUT). check_abort = false: time limit only.
+// limit_ns (then raises DG_ETIMEOUT). check_abort = false: time limit only.
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_s,
-                                       int* status, bool check_abort) {
+                                       int* status, unsigned long long limit_ns, bool check_abort) {
   const uint64_t t0 = gtimer();
   for (uint32_t k = 1;; ++k) {
     if (mbar_try(bar, parity)) return true;
     if ((k & 63) == 0) {
       if (check_abort && *abort_s) return false;
-      if (gtimer() - t0 > kWaitNs) {
+      if (gtimer() - t0 > limit_ns) {
         *abort_s = 1;
         raise_status(status, DG_ETIMEOUT);
         return false;
@@ -352,7 +355,7 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile 
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Sync& sy, const Args& a,
                                      bool check_abort = true) {
-  return mbar_try(bar, parity) || wait_slow(bar, parity, &sy.abort, a.w.c.status, check_abort);
+  return mbar_try(bar, parity) || wait_slow(bar, parity, &sy.abort, a.w.c.status, a.wait_ns, check_abort);
 }
 
 // A whole warp waits, every lane for itself: with one lane waiting and the others
@@ -1024,7 +1027,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sy.p_full[bar]);
+        if (lane == 0 && gt + 1 != a.stall) mbar_arrive(&sy.p_full[bar]);
       }
       if (!ok) break;
       // ---------------------------------------------------------- the segment's result
@@ -1449,6 +1452,10 @@ __global__ void __launch_bounds__(256) k_join(const __grid_constant__ Args a, in
 // ---------------------------------------------------------------------------
 size_t al(size_t x) { return (x + 255) / 256 * 256; }
 
+// Failure-path testing, for every later call of the process.
+std::atomic<unsigned long long> wait_ns{kWaitNs};
+std::atomic<uint32_t> stall{0};
+
 struct Plan {
   int dp, nt, rows;            // padded head_dim, row tiles per item, rows kept per piece
   size_t o, ml, open, total;   // scratch offsets and size
@@ -1549,6 +1556,14 @@ extern "C" size_t dg_cache_attention_scratch_bytes(const dg_kv_cache* cache, con
   return attn::make_plan(*cache, *batch, q_heads).total;
 }
 
+extern "C" int dg_cache_attention_inject_stall(int64_t wait_limit_ns, int32_t stall) {
+  if (wait_limit_ns < 0 || wait_limit_ns > 60ll * 1000000000ll || stall < 0)
+    return fail(DG_EINVAL, "wait limit must lie in [0, 60 s] and stall be >= 0");
+  attn::wait_ns = wait_limit_ns ? (unsigned long long)wait_limit_ns : attn::kWaitNs;
+  attn::stall = (uint32_t)stall;
+  return DG_OK;
+}
+
 extern "C" int dg_cache_attention(const dg_kv_cache* cache, const dg_kv_batch* batch, int32_t q_heads,
                                   const void* q, int64_t q_ts, int64_t q_hs, float scale, int32_t mask,
                                   const uint32_t* tree_mask, int32_t mask_words, void* out, float* lse,
@@ -1580,7 +1595,8 @@ extern "C" int dg_cache_attention(const dg_kv_cache* cache, const dg_kv_batch* b
   const Args a{{*cache, *batch}, static_cast<const __nv_bfloat16*>(q), q_ts, q_hs, q_heads,
                (int)G, mul_of(G), mul_of(ps), 31 + log_of(G), 31 + log_of(ps), scale * 1.4426950408889634f, mask, tree_mask, mask_words,
                static_cast<__nv_bfloat16*>(out), lse, reinterpret_cast<float*>(sc + p.o),
-               reinterpret_cast<float2*>(sc + p.ml), reinterpret_cast<Open*>(sc + p.open), p.rows, 0, 0};
+               reinterpret_cast<float2*>(sc + p.ml), reinterpret_cast<Open*>(sc + p.open), p.rows, 0, 0,
+               wait_ns.load(std::memory_order_relaxed), stall.load(std::memory_order_relaxed)};
   const int ctas = std::min(sms, kMaxCtas);
   const bool f8 = cache->format == DG_KV_E4M3;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
