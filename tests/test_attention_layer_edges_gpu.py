@@ -294,3 +294,28 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(fmt, D, G, 
             assert torch.equal(l.view(torch.int32), lse.view(torch.int32))
     finally:
         dg.dg_cache_attention_inject_stall(0, 0)
+
+
+@pytest.mark.parametrize("fmt", [dg.DG_KV_BF16, dg.DG_KV_E4M3])
+def test_a_long_search_for_infinities_is_no_stall(fmt):
+    """Searching a long tree's values for infinities takes each row longer than the (shortened) limit of a
+    wait, and is progress all the same."""
+    n = 4000
+    s = Setup16([(0, n), (0, n)], fmt, 1, 64, 64, seed=2)
+    q = _tokens_q(s, 1)
+    _infinite(s, "v", 0, 0, 7)
+    _infinite(s, "v", 1, n - 1, 7)
+    bits = np.packbits(np.tri(n, 4000, dtype=np.uint8), axis=1, bitorder="little").view(np.uint32)
+    bits = np.concatenate([bits, bits])
+    tree = torch.from_numpy(bits.view(np.int32)).cuda()
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    try:
+        dg.dg_cache_attention_inject_stall(1_000_000, 0)
+        start.record()
+        out, lse = s.cache.attend(q, s.batch, dg.DG_MASK_TREE, tree=tree)
+        end.record()
+        s.cache.check()
+    finally:
+        dg.dg_cache_attention_inject_stall(0, 0)
+    assert start.elapsed_time(end) > 2                  # ms: the search did take longer than the limit
+    _check_attention(s, q, "tree", 0.125, out, lse, bits, rows=[0, 1, 77, 1999, 3000, n - 2, n - 1])

@@ -331,22 +331,35 @@ struct Sync {
   uint64_t raw[8], taken[4];       // e4m3: a tile's codes have landed, and have been converted (bf16: a value
                                    // tile to be cleaned has landed)
   uint8_t exps[4][128];            // their rows' exponents
+  uint64_t busy;                   // when the search for infinities last said that it goes on
   uint32_t tmem;
   int abort, nonfinite;
   Start start;
 };
 
+// A CTA's shared memory, aligned: query tiles, ring, codes; then its Sync.
+__device__ __forceinline__ unsigned char* tiles() {
+  extern __shared__ unsigned char smem_raw[];
+  return reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+}
+template <class S>
+__device__ __forceinline__ Sync& sync_of() {
+  return *reinterpret_cast<Sync*>(tiles() + S::NT * S::QTILE + S::SL * S::SLOT + S::AHEAD * S::RAW);
+}
+
 // Bounded wait on an mbarrier phase; gives up on the CTA's abort flag or after
-// limit_ns (then raises DG_ETIMEOUT). check_abort = false: time limit only.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_s,
-                                       int* status, unsigned long long limit_ns, bool check_abort) {
+// limit_ns in which nothing was said to go on (then raises DG_ETIMEOUT).
+// check_abort = false: time limit only.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Sync& sy, int* status,
+                                       unsigned long long limit_ns, bool check_abort) {
   const uint64_t t0 = gtimer();
   for (uint32_t k = 1;; ++k) {
     if (mbar_try(bar, parity)) return true;
     if ((k & 63) == 0) {
-      if (check_abort && *abort_s) return false;
-      if (gtimer() - t0 > limit_ns) {
-        *abort_s = 1;
+      if (check_abort && *(volatile int*)&sy.abort) return false;
+      const uint64_t since = max(t0, *(volatile uint64_t*)&sy.busy);   // (may be later than this thread's clock)
+      if ((int64_t)(gtimer() - since) > (int64_t)limit_ns) {
+        *(volatile int*)&sy.abort = 1;
         raise_status(status, DG_ETIMEOUT);
         return false;
       }
@@ -355,7 +368,7 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile 
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Sync& sy, const Args& a,
                                      bool check_abort = true) {
-  return mbar_try(bar, parity) || wait_slow(bar, parity, &sy.abort, a.w.c.status, a.wait_ns, check_abort);
+  return mbar_try(bar, parity) || wait_slow(bar, parity, sy, a.w.c.status, a.wait_ns, check_abort);
 }
 
 // A whole warp waits, every lane for itself: with one lane waiting and the others
@@ -774,42 +787,67 @@ __device__ __forceinline__ float logit_of(const Args& a, const __nv_bfloat16* q,
   return z * a.scale_log2;
 }
 
-// o (columns d .. d + 3 of the sum of output row `orow`, one of the sequence's) and
-// the infinities and NaN among the values that it sees in the segment's keys from
-// position `from` on, where clean_rows has left them out. They are added as they
-// are, whatever their positive weight; times a weight of zero (a logit of minus
-// infinity) an infinity is NaN.
+// Adds to a warp's rows of O (in TMEM; orow: a lane's output row, one of the
+// sequence's, or -1) the infinities and NaN among the values that each sees in the
+// segment's keys from position `from` on, where clean_rows has left them out. They
+// are added as they are, whatever their positive weight; times a weight of zero (a
+// logit of minus infinity) an infinity is NaN. (A long tree's search can outlast
+// the limit of the waits behind it, so it says that it goes on.)
 template <class S, typename W>
-__device__ __noinline__ float4 with_not_finite(const W w, const uint32_t* tree, int orow, int d, int64_t from, float4 o) {
+__device__ __noinline__ void add_not_finite(const W w, int orow, int64_t from, uint32_t t_o) {
   const Args& a = w.a;
-  if (d >= a.w.c.head_dim) return o;
-  const int token = orow / a.q_heads, i = token - w.t0;
+  const int D = a.w.c.head_dim, token = orow / a.q_heads, i = token - w.t0;
+  const uint32_t* tree = a.mask == DG_MASK_TREE ? a.tree + (int64_t)token * a.words : nullptr;
   const __nv_bfloat16* q = a.q + (int64_t)token * a.q_ts + (int64_t)(orow - token * a.q_heads) * a.q_hs;
-  float x[4] = {0.f, 0.f, 0.f, 0.f};
   const int64_t end = min(w.keys(), (int64_t)w.te * S::BN);
-  for (int64_t j = max(from, (int64_t)w.tb * S::BN); j < end; ++j) {
-    if (!(seen(w, tree, i, j) & 1)) continue;
-    const int row = cache_row(a, a.w.b.page_table + (int64_t)w.b * a.w.b.table_stride, j, w.h);
-    if (row < 0) continue;
-    const int64_t at = (int64_t)row * a.w.c.head_dim + d;
-    uint2 c;                                         // the four values as they enter the products
-    if constexpr (S::F8) {
-      const uint32_t codes = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.w.c.v) + at);
-      const float scale = exponent_scale(a.w.c.v_exp[row]);
-      c = make_uint2(codes_to_bf16(codes, scale), codes_to_bf16(codes >> 16, scale));
-    } else {
-      c = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.w.c.v) + at);
-    }
-    if (only_finite(c.x) == c.x && only_finite(c.y) == c.y) continue;
-    const bool zero = logit_of<S>(a, q, row) == -INFINITY;
+  for (int d = 0; d < D; d += 16) {                  // (head_dim is a multiple of 16)
+    uint32_t o[16];
+    __syncwarp();
+    tmem_ld16_issue(t_o + d, o);
+    tmem_ld16_wait(o);
+    float x[16];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t half = (k < 2 ? c.x : c.y) >> (16 * (k & 1)) & 0xffffu;
-      if (!finite_bf16(half)) x[k] += zero ? NAN : __uint_as_float(half << 16);
+    for (int k = 0; k < 16; ++k) x[k] = 0.f;
+    for (int64_t j = orow < 0 ? end : max(from, (int64_t)w.tb * S::BN); j < end; ++j) {
+      if ((j & 63) == 0) *(volatile uint64_t*)&sync_of<S>().busy = gtimer();
+      if (!(seen(w, tree, i, j) & 1)) continue;
+      const int row = cache_row(a, a.w.b.page_table + (int64_t)w.b * a.w.b.table_stride, j, w.h);
+      if (row < 0) continue;
+      const int64_t at = (int64_t)row * D + d;
+      uint32_t c[8];                                 // the values as they enter the products
+      if constexpr (S::F8) {
+        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.w.c.v) + at);
+        const uint32_t codes[4] = {v.x, v.y, v.z, v.w};
+        const float scale = exponent_scale(a.w.c.v_exp[row]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          c[2 * k] = codes_to_bf16(codes[k], scale);
+          c[2 * k + 1] = codes_to_bf16(codes[k] >> 16, scale);
+        }
+      } else {
+        const uint4* v = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.w.c.v) + at);
+        const uint4 v0 = v[0], v1 = v[1];
+        c[0] = v0.x; c[1] = v0.y; c[2] = v0.z; c[3] = v0.w;
+        c[4] = v1.x; c[5] = v1.y; c[6] = v1.z; c[7] = v1.w;
+      }
+      bool fine = true;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) fine = fine && only_finite(c[k]) == c[k];
+      if (fine) continue;
+      const bool zero = logit_of<S>(a, q, row) == -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const uint32_t half = c[k >> 1] >> (16 * (k & 1)) & 0xffffu;
+        if (!finite_bf16(half)) x[k] += zero ? NAN : __uint_as_float(half << 16);
+      }
     }
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (x[k] != 0.f) o[k] = __float_as_uint(__uint_as_float(o[k]) + x[k]);
+    __syncwarp();
+    tmem_st16(t_o + d, o);
   }
-  return make_float4(x[0] == 0.f ? o.x : o.x + x[0], x[1] == 0.f ? o.y : o.y + x[1],
-                     x[2] == 0.f ? o.z : o.z + x[2], x[3] == 0.f ? o.w : o.w + x[3]);
+  tmem_st_wait();
 }
 
 // A 4 x 4 transposition of 16-byte pieces over each four lanes: lane q of four
@@ -840,12 +878,10 @@ template <class S>
 __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap k_map,
                                                            const __grid_constant__ CUtensorMap v_map,
                                                            const __grid_constant__ CUtensorMap q_map) {
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem =
-      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* smem = tiles();
   unsigned char* ring = smem + S::NT * S::QTILE;
   unsigned char* codes = ring + S::SL * S::SLOT;
-  Sync& sy = *reinterpret_cast<Sync*>(codes + S::AHEAD * S::RAW);
+  Sync& sy = sync_of<S>();
   static_assert(sizeof(Sync) <= 1024 && S::SL <= 8 && S::N_LOAD <= 8 && S::AHEAD <= 4, "barriers");
   int64_t* pref = reinterpret_cast<int64_t*>(ring);
   constexpr int ROWS = S::NT * 128, BN = S::BN;
@@ -865,6 +901,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     for (int x = 0; x < 8; ++x) mbar_init(&sy.raw[x], S::F8 ? 1 + BN / 8 : 1);
     for (int x = 0; x < S::AHEAD; ++x) mbar_init(&sy.taken[x], S::TEAM);
     sy.abort = 0;
+    sy.busy = 0;
     sy.nonfinite = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -1033,12 +1070,13 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       // ---------------------------------------------------------- the segment's result
       if (!pv_done(gt - 1)) { ok = false; break; }
       const bool whole = w.tb == 0 && w.te == w.T;
-      const bool fix = a.mask != DG_MASK_FULL && *(volatile int*)&sy.nonfinite;
+      const bool fix = a.mask != DG_MASK_FULL && __any_sync(0xffffffffu, *(volatile int*)&sy.nonfinite);
       const int piece = blockIdx.x * 2 + (w.tb == 0 ? 1 : 0);
       const int orow = (w.t0 + i) * a.q_heads + w.h * a.G + g;
       const int64_t prow = (int64_t)piece * a.rows + r;
       tc_fence_after();
       if (any) {
+        if (fix) add_not_finite<S>(w, valid ? orow : -1, w.clear() / BN * BN, t_o);
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
         // stores by fours of lanes, 64 contiguous bytes of a row each
         const int four = lane & ~3, q = lane & 3;
@@ -1047,15 +1085,6 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           float o[32];
           __syncwarp();                               // the lanes part below; TMEM loads take all of them
           tmem_ld32(t_o + c * 32, o);
-          if (fix && valid) {
-#pragma unroll
-            for (int d = 0; d < 32; d += 4) {
-              const float4 u = with_not_finite<S>(w, tree, orow, c * 32 + d, w.clear() / BN * BN,
-                                                  make_float4(o[d], o[d + 1], o[d + 2], o[d + 3]));
-              o[d] = u.x; o[d + 1] = u.y; o[d + 2] = u.z; o[d + 3] = u.w;
-            }
-          }
-          __syncwarp();
           if (whole) {
             uint4 v[4];
 #pragma unroll
