@@ -319,3 +319,31 @@ def test_a_long_search_for_infinities_is_no_stall(fmt):
         dg.dg_cache_attention_inject_stall(0, 0)
     assert start.elapsed_time(end) > 2                  # ms: the search did take longer than the limit
     _check_attention(s, q, "tree", 0.125, out, lse, bits, rows=[0, 1, 77, 1999, 3000, n - 2, n - 1])
+
+
+def test_check_waits_for_calls_of_other_streams():
+    """A bad page met on a side stream, behind work that takes a while."""
+    s = Setup([(40, 3)], dg.DG_KV_BF16, 1, 64, 16, seed=1)
+    q = _tokens_q(s, 2)
+    x = torch.randn(8192, 8192, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def work():
+        y = x
+        for _ in range(20):
+            y = y @ y
+            y /= y.norm()
+        s.cache.attend(q, s.batch, dg.DG_MASK_CAUSAL)
+
+    with torch.cuda.stream(side):                       # allocations, which would wait, made beforehand
+        work()
+    s.cache.check()
+    s.table[0, 1] = -1
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        work()
+    with pytest.raises(dg.DgError) as e:
+        s.cache.check()
+    assert e.value.code == dg.DG_EINVAL
+    torch.cuda.synchronize()

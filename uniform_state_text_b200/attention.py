@@ -153,7 +153,9 @@ class KVCache:
         return cls(*kv, *(torch.zeros(shape[:3], dtype=torch.uint8, device=device) for _ in "kv"))
 
     def check(self) -> None:
-        """Raise DgError if a call met a bad page or a wait ran out (synchronises)."""
+        """Raise DgError if a call met a bad page or a wait ran out. Waits for the whole device: calls
+        may have run on any of its streams. The first error stays until status is set to zero."""
+        torch.cuda.synchronize(self.index)
         code = int(self.status.item())
         if code:
             raise DgError(code, "a cache call met a page or position outside the cache, or a wait ran out")
