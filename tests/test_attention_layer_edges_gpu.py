@@ -6,7 +6,7 @@ import torch
 
 import uniform_state_text_b200 as dg
 from oracle import attention as A
-from test_attention_layer_gpu import MASKS, U32, Setup, _check_attention, _tokens_q, _tree, f64
+from test_attention_layer_gpu import MASKS, U16, U32, Setup, _check_attention, _check_norm, _tokens_q, _tree, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -347,3 +347,24 @@ def test_check_waits_for_calls_of_other_streams():
         s.cache.check()
     assert e.value.code == dg.DG_EINVAL
     torch.cuda.synchronize()
+
+
+# ----------------------------------------------------------------------------- norms of very large and small rows
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 1e-33, 1e30])
+@pytest.mark.parametrize("D,rot,interleaved", [(64, 32, False), (128, 128, True), (256, 64, False)])
+def test_norms_of_rows_whose_squares_leave_fp32(D, rot, interleaved, eps, dt):
+    """Rows from 1e-38 to 1e38, side by side: the squares' sum is far beyond fp32 or vanishes in it."""
+    sizes = [1.0, 1e-38, 1e38, 1e-25, 1e25, 1e-20, 3e19, 1e-15, 1e-12, 1e15, 1e-30, 1e18]
+    g = torch.Generator("cuda").manual_seed(D)
+    x = torch.rand(7, 2 * len(sizes), D, generator=g, device="cuda") * 2 - 1
+    x *= torch.tensor(sizes + sizes[::-1], device="cuda")[:, None]
+    x = x.to(dt)
+    w = (1 + 0.3 * torch.randn(D, generator=g, device="cuda")).to(dt)
+    pos, freq = torch.arange(7, device="cuda").int(), dg.rope_frequencies(rot)
+    n = len(sizes)
+    q, k = dg.qk_norm_rope(x[:, :n], x[:, n:], w, None, pos, freq, interleaved=interleaved, eps=eps)
+    ulp = U16 if dt == torch.bfloat16 else 0.0
+    eps = float(np.float32(eps))
+    _check_norm(x[:, :n], q, w, pos, freq, interleaved, eps, 0.0, ulp)
+    _check_norm(x[:, n:], k, None, pos, freq, interleaved, eps, 0.0, ulp)

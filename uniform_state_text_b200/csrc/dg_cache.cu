@@ -110,83 +110,137 @@ __device__ __forceinline__ void sincos_turns(uint64_t phase, float* s, float* c)
   sincospif((float)(int32_t)(uint32_t)(phase >> 32) * 4.656612873077392578125e-10f, s, c);
 }
 
+constexpr float kLeast = 0x1p-100f, kMost = 0x1p120f;   // mean squares between them are right in fp32
+
+// Over the LPR lanes of each row, the same in all of them.
+template <int LPR>
+__device__ __forceinline__ float sum_of_squares(const float* v) {
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+#pragma unroll
+  for (int m = LPR / 2; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+  return ss;
+}
+
+// Where a lane's 8 elements of a row lie: 4 pairs of the rotation, (4 l, 4 l + half)
+// or 8 neighbours, or else 8 elements behind rot, so that none changes lanes.
+template <bool INTERLEAVED>
+struct Place {
+  int sub, x0, x1;             // the lane within its row's; elements x0 .. + 3 and x1 .. + 3
+  bool turn, in;
+  __device__ __forceinline__ Place(const NormArgs& a, int lpr) {
+    sub = threadIdx.x % lpr;
+    turn = sub * 8 < a.rot;
+    in = sub * 8 < a.D;
+    x0 = !INTERLEAVED && turn ? sub * 4 : sub * 8;
+    x1 = !INTERLEAVED && turn ? a.rot / 2 + sub * 4 : x0 + 4;
+  }
+};
+
+template <typename T, bool I>
+__device__ __forceinline__ void load_row(const NormArgs& a, const Place<I>& at, int t, int h, float* v) {
+  const T* src = h < a.qh ? static_cast<const T*>(a.q) + t * a.q_ts + h * a.q_hs
+                          : static_cast<const T*>(a.k) + t * a.k_ts + (h - a.qh) * a.k_hs;
+  load4(src + at.x0, v);
+  load4(src + at.x1, v + 4);
+}
+
+// v rs weight, rotated, to the output. sh: weights of q and k, cosines, sines; tok:
+// the token within the block's.
+template <typename T, bool I>
+__device__ __forceinline__ void finish_row(const NormArgs& a, const Place<I>& at, const float* sh, int t, int tok, int h,
+                                           const float* v, float rs) {
+  const bool is_q = h < a.qh;
+  const int half = a.rot / 2;
+  const float* w = is_q ? sh : sh + a.D;
+  const float* cs = sh + 2 * a.D;
+  const float* sn = cs + a.tpb * half;
+  const float4 w0 = *reinterpret_cast<const float4*>(w + at.x0), w1 = *reinterpret_cast<const float4*>(w + at.x1);
+  float y[8] = {v[0] * rs * w0.x, v[1] * rs * w0.y, v[2] * rs * w0.z, v[3] * rs * w0.w,
+                v[4] * rs * w1.x, v[5] * rs * w1.y, v[6] * rs * w1.z, v[7] * rs * w1.w};
+  if (at.turn) {
+    const float4 c = *reinterpret_cast<const float4*>(cs + tok * half + at.sub * 4);
+    const float4 s = *reinterpret_cast<const float4*>(sn + tok * half + at.sub * 4);
+    const float cc[4] = {c.x, c.y, c.z, c.w}, sc[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float& ya = y[I ? 2 * j : j];
+      float& yb = y[I ? 2 * j + 1 : j + 4];
+      const float p = ya * cc[j] - yb * sc[j];
+      yb = yb * cc[j] + ya * sc[j];
+      ya = p;
+    }
+  }
+  T* dst = is_q ? static_cast<T*>(a.qo) + ((int64_t)t * a.qh + h) * a.D
+                : static_cast<T*>(a.ko) + ((int64_t)t * a.kh + h - a.qh) * a.D;
+  store4(dst + at.x0, y);
+  store4(dst + at.x1, y + 4);
+}
+
 // A block takes `hpb` heads of `tpb` tokens. Their cosines and sines, which cost
 // as much as the rest of several heads, are worked out once into shared memory,
 // and so are the weights in fp32; then a group of LPR lanes takes a row at a
-// time. A lane has 4 pairs of the rotation, (4 l, 4 l + half) or 8 neighbours,
-// or else 8 elements behind rot, so that no element changes lanes.
+// time.
 //
 // 16384 tokens of 24 heads of 128, bf16: 53 us, 3.8 TB/s; bound by the
 // instructions of a row (about 110 of a warp for 512 bytes in and out). Two rows
 // in flight took 62 us (fewer warps fit), the sines of a lane's own heads in
 // registers 88.
 template <typename T, int LPR, bool INTERLEAVED>
-__global__ void __launch_bounds__(THREADS) k_norm_rope(const NormArgs a) {
-  extern __shared__ float sh[];
+__global__ void __launch_bounds__(THREADS) k_norm_rope(const __grid_constant__ NormArgs a) {
+  extern __shared__ float sh[];                     // weights [2][D], cosines [tpb][half], sines
   constexpr int GROUPS = THREADS / LPR;
   const int half = a.rot / 2;
   const int t0 = blockIdx.x * a.tpb, nt = min(a.tpb, a.tokens - t0);
   const int h0 = blockIdx.y * a.hpb, nh = min(a.hpb, a.qh + a.kh - h0);
-  float* wq = sh;                                   // [D]
-  float* wk = wq + a.D;                             // [D]
-  float* cs = wk + a.D;                             // [tpb][half]
-  float* sn = cs + a.tpb * half;
-  const int sub = threadIdx.x % LPR, nr = nt * nh;
-  const bool turn = sub * 8 < a.rot, in = sub * 8 < a.D;
-  const int x0 = !INTERLEAVED && turn ? sub * 4 : sub * 8;          // elements x0 .. + 3
-  const int x1 = !INTERLEAVED && turn ? half + sub * 4 : x0 + 4;    // and x1 .. + 3
+  const Place<INTERLEAVED> at(a, LPR);
+  const int nr = nt * nh;
   const uint32_t mul = nh > 1 ? 0xffffffffu / (uint32_t)nh + 1 : 0; // r / nh by the high half, exact for r < 2^16
   for (int x = threadIdx.x; x < 2 * a.D; x += THREADS) {
     const T* w = static_cast<const T*>(x < a.D ? a.wq : a.wk);
     sh[x] = (w ? to_f32(w[x < a.D ? x : x - a.D]) : 1.0f) + a.off;
   }
+  float* cs = sh + 2 * a.D;
   for (int x = threadIdx.x; x < nt * half; x += THREADS) {
     const int t = x / half, p = x - t * half;
-    sincos_turns((uint64_t)(int64_t)__ldg(a.pos + t0 + t) * turns_per_position(__ldg(a.freq + p)), &sn[x], &cs[x]);
+    sincos_turns((uint64_t)(int64_t)__ldg(a.pos + t0 + t) * turns_per_position(__ldg(a.freq + p)), &cs[a.tpb * half + x], &cs[x]);
   }
   __syncthreads();
   const float per = 1.0f / (float)a.D;
+  uint32_t far = 0;                                 // a bit for each of the (at most eight) rounds
   for (int r0 = 0; r0 < nr; r0 += GROUPS) {         // every lane of the block runs every round
     const int r = r0 + threadIdx.x / LPR;
-    const bool on = r < nr && in;
     const int tok = nh > 1 ? (int)__umulhi((uint32_t)r, mul) : r;
     const int h = h0 + r - tok * nh, t = t0 + tok;
-    const bool is_q = h < a.qh;
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (on) {
-      const T* src = is_q ? static_cast<const T*>(a.q) + t * a.q_ts + h * a.q_hs
-                          : static_cast<const T*>(a.k) + t * a.k_ts + (h - a.qh) * a.k_hs;
-      load4(src + x0, v);
-      load4(src + x1, v + 4);
-    }
-    float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
-#pragma unroll
-    for (int m = LPR / 2; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+    const bool on = r < nr && at.in;
+    if (on) load_row<T>(a, at, t, h, v);
+    const float mean = fmaf(sum_of_squares<LPR>(v), per, a.eps);
     if (!on) continue;
-    const float rs = rsqrtf(fmaf(ss, per, a.eps));  // 2 ulp
-    const float* w = is_q ? wq : wk;
-    const float4 w0 = *reinterpret_cast<const float4*>(w + x0), w1 = *reinterpret_cast<const float4*>(w + x1);
-    float y[8] = {v[0] * rs * w0.x, v[1] * rs * w0.y, v[2] * rs * w0.z, v[3] * rs * w0.w,
-                  v[4] * rs * w1.x, v[5] * rs * w1.y, v[6] * rs * w1.z, v[7] * rs * w1.w};
-    if (turn) {
-      const float4 c = *reinterpret_cast<const float4*>(cs + tok * half + sub * 4);
-      const float4 s = *reinterpret_cast<const float4*>(sn + tok * half + sub * 4);
-      const float cc[4] = {c.x, c.y, c.z, c.w}, sc[4] = {s.x, s.y, s.z, s.w};
+    if (mean > kLeast && mean < kMost) finish_row<T>(a, at, sh, t, tok, h, v, rsqrtf(mean));   // (rsqrtf: 2 ulp)
+    else far |= 1u << (r0 / GROUPS);
+  }
+  // Rows whose mean square (and eps) lies where squares or their sum may have left
+  // fp32's range: again with the row times a power of two, which a small row keeps
+  // and a large one gives back after its division. (A row with infinities or NaN, and
+  // one of zeros without eps, come out as by the formula.)
+  if (!__any_sync(0xffffffffu, far)) return;
+#pragma unroll 1
+  for (int r0 = 0; r0 < nr; r0 += GROUPS) {
+    const bool on = far >> (r0 / GROUPS) & 1;
+    const int r = r0 + threadIdx.x / LPR, tok = r / nh, h = h0 + r - tok * nh, t = t0 + tok;
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (on) load_row<T>(a, at, t, h, v);
+    const bool small = fmaf(sum_of_squares<LPR>(v), per, a.eps) <= kLeast;
+    const float s = small ? 0x1p100f : 0x1p-70f;
+    float u[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float& ya = y[INTERLEAVED ? 2 * j : j];
-        float& yb = y[INTERLEAVED ? 2 * j + 1 : j + 4];
-        const float p = ya * cc[j] - yb * sc[j];
-        yb = yb * cc[j] + ya * sc[j];
-        ya = p;
-      }
-    }
-    T* dst = is_q ? static_cast<T*>(a.qo) + ((int64_t)t * a.qh + h) * a.D
-                  : static_cast<T*>(a.ko) + ((int64_t)t * a.kh + h - a.qh) * a.D;
-    store4(dst + x0, y);
-    store4(dst + x1, y + 4);
+    for (int j = 0; j < 8; ++j) u[j] = v[j] * s;
+    const float rs = rsqrtf(fmaf(sum_of_squares<LPR>(u), per, a.eps * s * s));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = small ? u[j] : v[j] * rs * s;
+    if (on) finish_row<T>(a, at, sh, t, tok, h, v, small ? rs : 1.f);
   }
 }
 
