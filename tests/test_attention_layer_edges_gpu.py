@@ -368,3 +368,19 @@ def test_norms_of_rows_whose_squares_leave_fp32(D, rot, interleaved, eps, dt):
     eps = float(np.float32(eps))
     _check_norm(x[:, :n], q, w, pos, freq, interleaved, eps, 0.0, ulp)
     _check_norm(x[:, n:], k, None, pos, freq, interleaved, eps, 0.0, ulp)
+
+
+def test_norm_of_the_most_tokens():
+    """2^31 - 1 tokens of one head of 8: a row that all read, 34 GB of them written."""
+    n = 2 ** 31 - 1
+    x = torch.randn(1, 1, 8, device="cuda").bfloat16()
+    out = torch.zeros(n, 8, dtype=torch.bfloat16, device="cuda")
+    dg.dg_qk_norm_rope(n, 1, 0, 8, 0, False, dg.DG_BF16, x.data_ptr(), 0, 0, 0, 0, 0, 0, 0, 0.0, 1e-6, 0, 0,
+                       out.data_ptr(), 0, torch.cuda.current_stream().cuda_stream)
+    want, _ = dg.qk_norm_rope(x, x[:, :0], None, None, torch.zeros(1, dtype=torch.int32, device="cuda"),
+                              dg.rope_frequencies(0))
+    for at in (0, n // 2, n - 33, n - 1):
+        assert torch.equal(out[at], want[0, 0])
+    assert (out[::4097] == want[0, 0]).all()
+    del out
+    torch.cuda.empty_cache()

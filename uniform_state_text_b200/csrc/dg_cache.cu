@@ -485,7 +485,7 @@ extern "C" int dg_qk_norm_rope(int32_t tokens, int32_t q_heads, int32_t k_heads,
     a.hpb = (int)std::min<int64_t>(heads, want);
     a.tpb = (int)std::min<int64_t>(std::max<int64_t>(1, want / heads), tokens);
     a.tpb = std::min(a.tpb, 32);
-    const dim3 grid((unsigned)((tokens + a.tpb - 1) / a.tpb), (unsigned)((heads + a.hpb - 1) / a.hpb));
+    const dim3 grid((unsigned)(((int64_t)tokens + a.tpb - 1) / a.tpb), (unsigned)((heads + a.hpb - 1) / a.hpb));
     const size_t smem = sizeof(float) * (2 * head_dim + a.tpb * rot_dim);   // at most 34 KB
     return by_type(dtype, [&](auto t) {
       using T = decltype(t);
