@@ -1283,7 +1283,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     }
   } else {
     // ---------------------------------------------------------------- MMA
-    // (the warp waits together, lane 0 issues)
+    // (the warp waits together, one elected lane issues)
     constexpr uint32_t id_s = idesc_bf16(128, BN, 0), id_o = idesc_bf16(128, S::DP, 1);
     const uint32_t q0 = smem_u32(smem), ring0 = smem_u32(ring);
     uint32_t gt = 0, seg = 0;                         // key tiles and segments so far; tile k's keys and values
@@ -1297,6 +1297,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
     const uint32_t tm = uniform(tmem);
     const uint64_t qd = sdesc(uniform(q0), 16, 1024);
     const uint64_t kd = sdesc(uniform(ring0), 16, 1024), vd = sdesc(uniform(ring0), BN * 128, 1024);
+    // Products run in the order of their issue only where accumulator and shape are
+    // the same. S of a key tile goes where P of an earlier one lies, so it is issued
+    // when that tile's P V, which reads it, is done (by issue order alone the prompt
+    // took 322 us for 326, canvases over a bf16 cache 92 for 95; one row tile, whose
+    // buffers alternate, no less).
+    auto pv_done = [&](uint32_t k, int x) { return wait_warp(&sy.o_done[4 * x + (k & 3)], (k >> 2) & 1, sy, a); };
     auto scores = [&](uint32_t k, int x, bool last) {   // S = Q(x) K^T of key tile k; the last of a segment frees Q
       tc_fence_after();
       const uint64_t b = kd + uniform((2 * k) % S::SL) * (uint64_t)(S::SLOT / 16);
@@ -1326,14 +1332,19 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
       }
       __syncwarp();
     };
+    constexpr uint32_t kBack = S::NT == 2 ? 1 : 2;    // key tiles since an S buffer was last used
     for (; w.more() && ok; w.next(), ++seg) {
       if (!wait_warp(&sy.q_full, seg & 1, sy, a) || !slot_full(2 * gt)) { ok = false; break; }
       const int n = w.te - w.tb;
 #pragma unroll
-      for (int x = 0; x < S::NT; ++x) scores(gt, x, n == 1);
+      for (int x = 0; x < S::NT; ++x) {
+        if (gt >= kBack && !pv_done(gt - kBack, x)) { ok = false; break; }
+        scores(gt, x, n == 1);
+      }
+      if (!ok) break;
       for (int t = 0; t < n && ok; ++t, ++gt) {
         if (S::NT == 1 && t + 1 < n) {                  // the next S has a buffer of its own
-          if (!slot_full(2 * gt + 2)) { ok = false; break; }
+          if ((gt + 1 >= kBack && !pv_done(gt + 1 - kBack, 0)) || !slot_full(2 * gt + 2)) { ok = false; break; }
           scores(gt + 1, 0, t + 2 == n);
         }
 #pragma unroll
@@ -1345,7 +1356,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) k_attend(const __grid_constant_
           }
           sums(gt, x, t == 0);
           if (S::NT == 2 && t + 1 < n) {
-            if (x == 0 && !slot_full(2 * gt + 2)) { ok = false; break; }
+            if ((x == 0 && !slot_full(2 * gt + 2)) || !pv_done(gt, x)) { ok = false; break; }
             scores(gt + 1, x, t + 2 == n);
           }
         }
