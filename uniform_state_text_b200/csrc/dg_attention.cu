@@ -39,27 +39,32 @@
 // that one tile's softmax runs under the other's products; with NT = 1 there
 // are two S buffers and S of the next keys is issued before P V of these. (With
 // two buffers for each of two tiles, TMEM has room for 64 keys to a tile only:
-// the prompt below then took 456 us for 347, a tile's hand-overs costing as
-// much as with 128.)
+// the prompt below, when it took 347 us, then took 456, a tile's hand-overs
+// costing as much as with 128.)
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 over the
 // one in use (P then stays below 2^8, harmless in bf16 and fp32): the wait for
-// the previous P V and the pass over O are rare. Without that the prompt took
-// 333 us for 293.
+// the previous P V and the pass over O are rare. Without that the prompt takes
+// 359 us for 327, the canvases 144 for 136.
 //
 // Rounding: keys, values and queries enter the products as they are; P is
-// rounded to bf16, the tensor cores' operand type with V's range (2^-9 relative,
-// independent from key to key); S, m, l and O stay in fp32; the output is
-// rounded once.
+// rounded to bf16, the tensor cores' operand type with V's range (2^-8 relative
+// at most, independent from key to key); S, m, l and O stay in fp32; the output
+// is rounded once.
 //
-// Measured on B200 (calls in turn on the device, two sets of inputs):
-//   one token, 131072 bf16 keys, 8 x 2 heads of 128: 96 us, 5.6 TB/s of the 6.55
+// Measured on B200 (replays of a captured graph, two sets of inputs in turn;
+// called one by one with inputs of their own each, the long sequence takes 106 us
+// and the prompt up to 338, the others as here):
+//   one token, 131072 bf16 keys, 8 x 2 heads of 128: 95 us, 5.6 TB/s of the 6.55
 //     that a copy reaches; bound by memory
-//   33 tokens, 2000 to 8000 e4m3 keys each, 8 x 4 heads of 128: 129 us, 2.2
+//   33 tokens, 2000 to 8000 e4m3 keys each, 8 x 4 heads of 128: 124 us, 2.3
 //     TB/s; bound by hand-overs between the warps, tile by tile
-//   4 canvases of 256, 8448 e4m3 keys, 4 x 2 heads of 256: 131 us, 540 TFLOP/s
-//   a prompt of 8192, 8 x 2 heads of 128: 290 us, 950 TFLOP/s; bound by the
-//     chain softmax - P V - S of each tile, the tensor cores busy half the time
+//   4 canvases of 256, 8448 e4m3 keys, 4 x 2 heads of 256: 137 us, 518 TFLOP/s;
+//     8 x 2 heads of 128: 117 us, over bf16 keys 95 (605 and 743 TFLOP/s)
+//   a prompt of 8192, 8 x 2 heads of 128: 327 us, 842 TFLOP/s (e4m3 keys 373);
+//     bound by the chain softmax - P V - S of each tile: S is read from TMEM
+//     twice, a row's 128 logits not fitting the registers of a softmax thread,
+//     and the tensor cores are busy half the time
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -83,7 +88,10 @@ using namespace tc;
 
 constexpr int kMaxCtas = 148;                 // scratch is laid out for at most this many
 constexpr int TMEM_COLS = 512;
-constexpr int kItem = 3;                      // an item's cost beside its key tiles, in key tiles
+// An item's cost beside its key tiles, in key tiles. (With 0 the prompt takes 351 us
+// for 322 and the single tokens 130 for 123, with 6 324 and 128; a single canvas,
+// where shares are of a tile or two, 22.5 for 23.6 with 0.)
+constexpr int kItem = 3;
 constexpr float kGrow = 8.0f;                 // log2 growth of a maximum that rescales O
 constexpr float kLarge = 16777216.0f;         // scaled logits of this size have steps of one and more
 constexpr unsigned long long kWaitNs = 2000000000ull;   // a wait's limit by default
@@ -140,9 +148,11 @@ struct Shape {
   static constexpr int SL = F8 ? (DP == 64 ? 6 : 4) : DP == 256 ? 4 : DP == 128 ? 5 : (NT == 2 ? 6 : 8);   // ring slots
   // Load warps. bf16: one per slot. e4m3: CW that convert, several to a tile, so
   // that a slot is not held longer than its share of the time, and two that
-  // bring the codes AHEAD tiles before. (The 33 single tokens above: 129 us with
-  // 4, 137 with 8, 215 with 2; the canvases, whose rows are twice as long: 146
-  // and 131.)
+  // bring the codes AHEAD tiles before. Eight warps pay where rows are of 256
+  // codes only (the canvases 136 us, with 4 146). Up to 128 they cost registers:
+  // with 4 and 8 the single tokens take 123 and 125 us, canvases of heads of 128
+  // 116 and 125, of 64 87 and 94, an e4m3 prompt 366 and 415. AHEAD is what
+  // shared memory leaves: 2 instead of 4 costs the single tokens 165 us for 123.
   static constexpr int CW = F8 ? (DP == 256 ? 8 : 4) : 0;
   static constexpr int TEAM = F8 ? CW / 2 : 1;         // half convert keys, half values
   static constexpr int N_LOAD = F8 ? CW : SL;
@@ -1502,8 +1512,10 @@ struct Plan {
 };
 
 // NT = 2 shares every key and value tile between two row tiles and needs more
-// than 128 rows to have a second one (the prompt above: 290 us, with NT = 1 386;
-// draft trees of 504 rows: 30.4 and 31.6); head_dim above 128 leaves TMEM and
+// than 128 rows to have a second one (the prompt above: 327 us, with NT = 1 370;
+// the canvases of heads of 128: 95 and 105, over e4m3 keys 117 and 128). Where a
+// CTA has a few tiles only, the two are close: one canvas over 2304 keys 23.8 and
+// 22.2, draft trees of 504 rows 31.7 and 30.4. head_dim above 128 leaves TMEM and
 // shared memory for one. The lengths are device data, so the rule goes by the
 // batch's average.
 Plan make_plan(const dg_kv_cache& c, const dg_kv_batch& b, int q_heads) {
@@ -1524,7 +1536,7 @@ template <class S>
 cudaError_t launch(Args a, int dev, int ctas, cudaStream_t s) {
   // TMA copies take runs of rows that lie together: a power of two that divides
   // page_size, at least 8 (one swizzle pattern, and the exponents' 8 bytes). Rows
-  // one by one instead: long sequence 151 us for 97, prompt 374 for 293
+  // one by one instead: long sequence 147 us for 95, prompt 376 for 327
   const dg_kv_cache& c = a.w.c;
   a.box = std::min(c.page_size & -c.page_size, S::BN);
   if (a.box < 8 || c.head_dim < 64 || c.pages == 0) a.box = 0;
@@ -1535,7 +1547,7 @@ cudaError_t launch(Args a, int dev, int ctas, cudaStream_t s) {
                 !tc_encode_2d_rows(&maps[1], c.v, c.head_dim, rows, S::F8 ? S::DP : 64, a.box, S::F8)))
     return cudaErrorInvalidValue;
   // queries: dimensions (column, head, token); a dimension of one takes any stride.
-  // (Row by row: prompt 313 us for 293.)
+  // (Row by row: prompt 342 us for 327, one canvas 25.6 for 23.8.)
   const int64_t hs = a.q_heads > 1 ? a.q_hs : c.head_dim, ts = a.w.b.tokens > 1 ? a.q_ts : a.q_heads * hs;
   a.q_box = a.G <= 32 && !(a.G & (a.G - 1)) && c.head_dim >= 64 && hs > 0 && ts > 0 && hs < (1ll << 38) && ts < (1ll << 38);
   alignas(64) CUtensorMap q_map = {};

@@ -2,11 +2,12 @@
 // (dg_qk_norm_rope), and the paged key/value cache's write and read
 // (dg_cache_write, dg_cache_read).
 //
-// All three are bound by memory: each element is read once and written once,
-// with a few operations between. A row (one token, one head) belongs to a
-// group of 8, 16 or 32 lanes (head_dim up to 64, 128, 256), 8 elements to a
-// lane, so that a row is one fully used memory transaction per lane and its
-// sums and maxima are a few shuffles; nothing passes through shared memory.
+// Each element is read once and written once, with a few operations between:
+// write and read are bound by memory, the norm by the instructions of its rows. A
+// row (one token, one head) belongs to a group of 8, 16 or 32 lanes (head_dim up
+// to 64, 128, 256), 8 elements to a lane, so that a row is one fully used memory
+// transaction per lane and its sums and maxima are a few shuffles; only the norm's
+// weights, cosines and sines pass through shared memory.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -183,10 +184,10 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, const Place<I>& at
 // and so are the weights in fp32; then a group of LPR lanes takes a row at a
 // time.
 //
-// 16384 tokens of 24 heads of 128, bf16: 53 us, 3.8 TB/s; bound by the
-// instructions of a row (about 110 of a warp for 512 bytes in and out). Two rows
+// 16384 tokens of 24 heads of 128, bf16: 52 us, 3.9 TB/s; bound by the
+// instructions of a row (about 115 of a warp for 512 bytes in and out). Two rows
 // in flight took 62 us (fewer warps fit), the sines of a lane's own heads in
-// registers 88.
+// registers 88. The second pass and the test for it cost 1.2 us.
 template <typename T, int LPR, bool INTERLEAVED>
 __global__ void __launch_bounds__(THREADS) k_norm_rope(const __grid_constant__ NormArgs a) {
   extern __shared__ float sh[];                     // weights [2][D], cosines [tpb][half], sines
@@ -297,7 +298,8 @@ __device__ __forceinline__ void write_row(const T* src, void* pages, uint8_t* ex
 }
 
 // A group of LPR lanes per (token, head): its key row and its value row. 22576
-// tokens of 4 heads of 256, fp32 to e4m3: 43 us, 5.3 TB/s.
+// tokens of 4 heads of 256, fp32 to e4m3: 42 us, 5.5 TB/s (called one by one 46);
+// bf16 to bf16 37 us, 5.0 TB/s.
 template <typename T, int LPR, bool F8>
 __global__ void __launch_bounds__(THREADS) k_cache_write(const __grid_constant__ WriteArgs a) {
   const KvView& w = a.w;
@@ -348,7 +350,8 @@ __device__ __forceinline__ void read_row(const void* pages, const uint8_t* exps,
 // A group of LPR lanes per head and TOK neighbouring tokens, whose rows lie
 // together in their page: one search for the sequence, and 2 TOK rows in flight.
 // 103000 tokens of 8 heads of 128, e4m3 to bf16: 133 us, 4.8 TB/s (1 token to a
-// group: 143; 8: 174).
+// group: 142; 8: 173), to fp32 177 us, 6.0 TB/s (187; 218); from a bf16 cache 156
+// us, 5.4 TB/s (150; 172).
 template <typename T, int LPR, bool F8, int TOK>
 __global__ void __launch_bounds__(THREADS) k_cache_read(const __grid_constant__ ReadArgs a) {
   const KvView& w = a.w;
@@ -478,7 +481,7 @@ extern "C" int dg_qk_norm_rope(int32_t tokens, int32_t q_heads, int32_t k_heads,
   const cudaError_t e = by_lanes(head_dim, [&](auto lpr) {
     constexpr int L = decltype(lpr)::value;
     // A block has about eight rounds of rows, so that the sines are shared by many
-    // rows (four: 70 us for 62 on the prompt above); with few tokens one or two,
+    // rows (four: 55.7 us for 52.1 on the prompt above); with few tokens one or two,
     // to fill the SMs.
     const int64_t round = THREADS / L, rows = (int64_t)tokens * heads;
     const int64_t want = rows >= 148 * 8 * round ? 8 * round : 2 * round;
