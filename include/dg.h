@@ -482,8 +482,9 @@ typedef struct dg_kv_cache {
  * of its cache; position p lies in page page_table[b][p / page_size]. Rows from
  * first[batch] on (padding) are left as they are. All arrays are device int32,
  * read when the kernels run, so that a captured graph can be replayed with new
- * lengths. Sequences may share pages that are only read; a page that a call
- * writes belongs to one sequence.
+ * lengths. Sequences may share pages that are only read, and name one more than
+ * once; a page that a call writes belongs to one sequence and stands in its
+ * table once (else two tokens would write one row).
  */
 typedef struct dg_kv_batch {
   const int32_t* page_table;  /* [batch][table_stride]                          */
